@@ -1,7 +1,10 @@
 /*
  * m3scan.h -- C ABI of libm3scan, the MI355X (gfx950) implementation of the
  * Mamba-3 sequence mixer: chunked prefill (m3_scan_fwd) and one autoregressive
- * step (m3_decode_step).
+ * step (m3_decode_step).  Beside it, for models that mix layers: the gated
+ * delta rule (m3_delta_fwd, m3_delta_step, m3_delta_bwd), and the operations on
+ * pools of either mixer's state records (m3_pool_copy, _fork, _compact, _free),
+ * each described at its declarations below.
  *
  * The operation (per batch row b and head h, t = 1..L):
  *
@@ -402,6 +405,168 @@ int m3_scan_supported(int64_t dstate, int64_t headdim, int64_t rank, int32_t chu
 
 /* 1 when (dstate, headdim, rank, io_dtype) is supported by m3_decode_step. */
 int m3_decode_supported(int64_t dstate, int64_t headdim, int64_t rank, int32_t io_dtype);
+
+/*
+ * Gated delta rule: the mixer whose state is corrected towards each token's
+ * value instead of added to.  Per batch row b (or packed sequence) and head h:
+ *
+ *   S_t = a_t S_{t-1} + k_t u_t^T,    a_t = exp(g_t)
+ *   u_t = beta_t (v_t - (a_t S_{t-1})^T k_t)
+ *   o_t = scale S_t^T q_t
+ *
+ * Data layout (dense, row-major, contiguous, 16-byte aligned):
+ *   q, k     [batch, seqlen, ngroups, dstate]     io dtype; head h reads group
+ *            h / (nheads / ngroups)
+ *   v, o     [batch, seqlen, nheads, headdim]     io dtype
+ *   g, beta  [batch, seqlen, nheads]              float32 (g: log decay, at
+ *            most 0 as a rule; values below -1024, -inf among them, decay to 0)
+ *   h        [batch, nheads, dstate, headdim]     float32: S, the state record
+ * l2norm 1: every row of q and of k is used as x / sqrt(sum(x^2) + norm_eps).
+ * Sizes: dstate 32, 64 or 128; headdim 32, 64, 96 or 128; ngroups 0 (one group
+ * per head) or a divisor of nheads.
+ *
+ * Options as in m3_scan_fwd:
+ *   cu_seqlens, max_seqlen   packed sequences (prefill and gradient): the token
+ *            arrays are [seqlen, ...] with seqlen the total, one state record
+ *            per sequence; 0 <= max_seqlen <= seqlen bounds every length.
+ *            Tokens outside the sequences: o is left as it was, gradients are 0
+ *   slots    int32 [batch] (prefill and step): row b's record is slot
+ *            slots[b] of a pool of nslots records, h_in and h_out (h) are then
+ *            [nslots, nheads, dstate, headdim].  A slot outside the pool (-1,
+ *            say, for a padding row) stands for no record: the row starts from
+ *            zero and leaves no state.  Of several rows that name one slot the
+ *            first has the record, the others' outputs are NaN.  Slots that no
+ *            row names are left as they were.
+ * Products run on bf16 matrix cores with float32 operands split into up to
+ * three bf16 values and float32 sums: states and gradients have float32's
+ * accuracy for both io dtypes.  NaN and Inf inputs propagate as in
+ * m3_scan_fwd (within their chunk of 64 tokens also to earlier tokens).
+ */
+typedef struct {
+    int64_t batch, seqlen, nheads, ngroups, headdim, dstate;
+    int32_t io_dtype;                 /* m3_dtype */
+    int32_t l2norm;                   /* 0 or 1 */
+    float scale, norm_eps;
+    const void *q, *k, *v;
+    const float *g, *beta;
+    const float *h_in;                /* NULL = zero state */
+    void *o;
+    float *h_out;                     /* NULL = not written; may be h_in */
+    const int32_t *cu_seqlens;        /* NULL = dense batch */
+    int64_t max_seqlen;
+    const int32_t *slots;             /* NULL = row b's record is record b */
+    int64_t nslots;
+    void *workspace;                  /* m3_delta_workspace_bytes, 256-byte aligned */
+    size_t workspace_bytes;
+} m3_delta_args;
+
+/* One token per row: q, k [batch, ngroups, dstate], v, o [batch, nheads,
+ * headdim], g, beta [batch, nheads]; h is updated in place. */
+typedef struct {
+    int64_t batch, nheads, ngroups, headdim, dstate;
+    int32_t io_dtype;
+    int32_t l2norm;
+    float scale, norm_eps;
+    const void *q, *k, *v;
+    const float *g, *beta;
+    float *h;
+    void *o;
+    const int32_t *slots;
+    int64_t nslots;
+} m3_delta_step_args;
+
+/* Gradient of sum(dout * o) + sum(dh_out * h_L) with respect to q, k, v, g,
+ * beta (as given: through l2norm) and h_in.  `in` as for the prefill, its o,
+ * h_out and slots NULL and its workspace m3_delta_bwd_workspace_bytes.  Outputs
+ * float32, the shapes of their inputs; a group's dq, dk sum those of its heads.
+ * dh_out NULL = zero, dh_in NULL = not wanted.  Every output is written;
+ * results do not change from call to call. */
+typedef struct {
+    m3_delta_args in;
+    const void *dout;                 /* io dtype, as o */
+    const float *dh_out;
+    float *dq, *dk, *dv, *dg, *dbeta;
+    float *dh_in;
+} m3_delta_bwd_args;
+
+m3_status m3_delta_fwd(const m3_delta_args *args, void *stream);
+m3_status m3_delta_step(const m3_delta_step_args *args, void *stream);
+m3_status m3_delta_bwd(const m3_delta_bwd_args *args, void *stream);
+/* Workspace bytes of the calls; 0 for arguments they would reject.  They
+ * depend on sizes, io dtype and on whether cu_seqlens is given. */
+size_t m3_delta_workspace_bytes(const m3_delta_args *args);
+size_t m3_delta_bwd_workspace_bytes(const m3_delta_bwd_args *args);
+/* 1 when (dstate, headdim, io_dtype) is in the compiled set of the three. */
+int m3_delta_supported(int64_t dstate, int64_t headdim, int32_t io_dtype);
+
+/*
+ * Pools of state records: `narrays` device arrays whose leading axis is the
+ * slot, row_bytes[i] bytes per slot in array i (a Mamba-3 record's h, B_prev
+ * and x_prev, the delta rule's h, or any other).  Which slots are in use is
+ * the caller's int32 live[slots] (0 = free); all decisions are taken on the
+ * device, in one stream order, without waiting for the host.
+ */
+#define M3_POOL_MAX_ARRAYS 8
+typedef struct {
+    int64_t slots;
+    int32_t narrays;
+    int32_t reserved;
+    void *data[M3_POOL_MAX_ARRAYS];
+    int64_t row_bytes[M3_POOL_MAX_ARRAYS];
+} m3_pool;
+
+/* Copy: record src_slot[i] of `src` to slot dst_slot[i] of `dst`, i < count, as
+ * if every source were read before any slot is written; of pairs that name one
+ * slot of dst the last wins.  src_slot[i] < 0: the slot is cleared.  Pairs with
+ * src_slot[i] >= src.slots or dst_slot[i] outside dst are left out.  dst may be
+ * src (all arrays the same): then a workspace of m3_pool_copy_workspace_bytes
+ * is needed; any other overlap is refused. */
+typedef struct {
+    m3_pool src, dst;
+    const int32_t *src_slot, *dst_slot;
+    int64_t count;
+    void *workspace;
+    size_t workspace_bytes;
+} m3_pool_copy_args;
+
+/* Fork: for each parents[i], in order, the lowest free slot gets a copy of
+ * record parents[i] (< 0: a cleared record) and is marked live; children[i] is
+ * that slot, or -1 where no slot is left or the parent is not live.  live_out
+ * may be live.  Workspace: 4 * count bytes. */
+typedef struct {
+    m3_pool pool;
+    const int32_t *live;
+    int32_t *live_out;
+    const int32_t *parents;
+    int32_t *children;
+    int64_t count;
+    void *workspace;
+    size_t workspace_bytes;
+} m3_pool_fork_args;
+
+/* Compact: with n live records, those in slots >= n move, in ascending order,
+ * to the free slots below n, ascending too; the others stay.  new_slot[s] =
+ * where slot s's record is now, -1 for a free slot; count (optional) = n;
+ * live_out (optional, may be live) = 1 below n, 0 from there.  Slots that were
+ * left keep their bytes.  Workspace: 4 * (slots + 1) bytes. */
+typedef struct {
+    m3_pool pool;
+    const int32_t *live;
+    int32_t *live_out;
+    int32_t *new_slot;
+    int32_t *count;
+    void *workspace;
+    size_t workspace_bytes;
+} m3_pool_compact_args;
+
+m3_status m3_pool_copy(const m3_pool_copy_args *args, void *stream);
+m3_status m3_pool_fork(const m3_pool_fork_args *args, void *stream);
+m3_status m3_pool_compact(const m3_pool_compact_args *args, void *stream);
+/* Free: live[list[i]] = 0, i < count; entries outside the pool are left out. */
+m3_status m3_pool_free(int32_t *live, int64_t slots, const int32_t *list, int64_t count, void *stream);
+/* 0 where src and dst are different pools, and for arguments that
+ * m3_pool_copy would reject. */
+size_t m3_pool_copy_workspace_bytes(const m3_pool_copy_args *args);
 
 /* Static description of a status code.  Never NULL. */
 const char *m3_status_string(m3_status status);

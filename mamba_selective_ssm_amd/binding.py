@@ -156,6 +156,19 @@ def load_library():
         lib.m3_last_hip_error.argtypes = []
         lib.m3_abi_version.restype = ctypes.c_int
         lib.m3_abi_version.argtypes = []
+        # the gated delta rule and the record pools (delta.py, pool.py)
+        for name in ("m3_delta_fwd", "m3_delta_step", "m3_delta_bwd", "m3_pool_copy", "m3_pool_fork",
+                     "m3_pool_compact"):
+            getattr(lib, name).restype = ctypes.c_int
+            getattr(lib, name).argtypes = [_vp, _vp]
+        for name in ("m3_delta_workspace_bytes", "m3_delta_bwd_workspace_bytes",
+                     "m3_pool_copy_workspace_bytes"):
+            getattr(lib, name).restype = ctypes.c_size_t
+            getattr(lib, name).argtypes = [_vp]
+        lib.m3_delta_supported.restype = ctypes.c_int
+        lib.m3_delta_supported.argtypes = [ctypes.c_int64, ctypes.c_int64, ctypes.c_int32]
+        lib.m3_pool_free.restype = ctypes.c_int
+        lib.m3_pool_free.argtypes = [_vp, ctypes.c_int64, _vp, ctypes.c_int64, _vp]
         _lib = lib
     return _lib
 

@@ -474,6 +474,10 @@ m3_status scratch_address(void* stream, void** out)
 
 }  // namespace
 
+namespace m3 {
+int record_hip(hipError_t e) { return hip_status(e); }
+}  // namespace m3
+
 extern "C" {
 
 size_t m3_scan_bwd_workspace_bytes(const m3_scan_bwd_args* a)

@@ -1,0 +1,210 @@
+// Gated delta rule: what its translation units share.
+//
+//   S_t = a_t S_{t-1} + k_t u_t^T,   u_t = beta_t (v_t - (a_t S_{t-1})^T k_t),
+//   o_t = scale S_t^T q_t,           a_t = exp(g_t)
+//
+// Chunked form, 64 tokens to a chunk.  With G_t the running sum of g inside the
+// chunk, S0 the state before it, e = exp(G), d_t = exp(G_last - G_t) and
+// D_ij = exp(G_i - G_j) for j <= i:
+//   (I + M) U = beta (V - e K S0),  M_ij = beta_i D_ij k_i.k_j  (j < i)
+//   O  = scale (e Q S0 + (D o Q K^T) U)
+//   S1 = exp(G_last) S0 + K^T (d U)
+// T = (I + M)^-1 does not depend on the state, so it is made for all chunks at
+// once; what is left for the walk over a sequence's chunks is three products a
+// chunk, each of them independent for every column of V.
+//
+// Matrix cores multiply bf16 operands here.  A float32 operand is the sum of
+// up to three bf16 values ("planes": its rounding, the rounding of what that
+// left, and once more), 24 bits together, and a product of two such operands
+// adds the plane products that float32 can still see: 3 where one side is an
+// exact bf16 value, 6 where both have three planes.  At 16x16x32 that is 48
+// and 96 cycles against 256 of the float32 instructions for the same product.
+#pragma once
+
+#include "m3_device.hpp"
+#include "m3_internal.hpp"
+
+namespace m3 {
+
+constexpr int kDC = 64;        // tokens per chunk
+constexpr int kDScal = 6;      // per-token factor rows that the chunk kernel leaves
+
+struct DeltaParams {
+    const void *q, *k, *v;
+    const float *g, *beta;
+    const float *h_in;
+    void *o;
+    float *h_out;
+    const int* cu;         // [rows + 1] packed-sequence offsets, or NULL
+    const int* slots;      // [rows] record of each row, or NULL (row b: record b)
+    int64_t nslots;        // records that h_in / h_out hold
+    int64_t L;             // tokens per row; packed: tokens in all
+    int64_t max_len;       // longest row
+    int rows, H, G;        // batch rows or sequences, heads, q/k head groups
+    int N, P;
+    float scale, eps;
+    int l2norm;
+    int nc;                // chunks of the longest row
+    // workspace, one entry per (chunk slot, head)
+    bf16* tf;              // T in operand order
+    bf16* af;              // scale D o Q K^T in operand order
+    float* sc;             // [kDScal][64] per-token factors
+};
+
+// Gradient: what the kernels add to the above.
+struct DeltaBwdParams {
+    DeltaParams f;
+    const void* dout;
+    const float* dh_out;
+    float *dq, *dk, *dv, *dg, *dbeta, *dh_in;
+    bf16* ttf;             // T^T in operand order
+    bf16* atf;             // A^T in operand order
+    float* S;              // [chunk][N][P] state before each chunk
+    float* dS;             // [chunk][N][P] adjoint of the state after each chunk
+    float* U;              // [chunk][64][P]
+    float* dR;             // [chunk][64][P]
+    float *dqe, *dke;      // [token][H][N] per-head gradients where heads share q and k, else dq and dk
+};
+
+hipError_t launch_delta_fwd(const DeltaParams& p, int io_dtype, hipStream_t stream);
+hipError_t launch_delta_bwd(const DeltaBwdParams& p, int io_dtype, hipStream_t stream);
+hipError_t launch_delta_step(const DeltaParams& p, int io_dtype, hipStream_t stream);
+
+constexpr bool delta_supported(int64_t N, int64_t P, int io_dtype)
+{
+    return (N == 32 || N == 64 || N == 128) && P >= 32 && P <= 128 && P % 32 == 0 && (io_dtype == 0 || io_dtype == 1);
+}
+
+// Planes of float32 operands on the state's path and on the output's path, and
+// of the io type's own values.  The output of a bf16 call is rounded to bf16
+// once more, so two planes (16 bits) are enough on its path.
+template <typename IO> struct DeltaPlanes;
+template <> struct DeltaPlanes<bf16> { static constexpr int io = 1, wide = 3, out = 2; };
+template <> struct DeltaPlanes<float> { static constexpr int io = 3, wide = 3, out = 3; };
+
+// Operand blocks of a lower triangular 64 x 64 matrix: 16 rows x 32 columns
+// each, block (w, kb) of row tile w at 0: (0,0) 1: (1,0) 2: (2,0) 3: (2,1)
+// 4: (3,0) 5: (3,1).  Of an upper triangular one (the transposes): 0: (0,0)
+// 1: (0,1) 2: (1,0) 3: (1,1) 4: (2,1) 5: (3,1).
+constexpr int kTriBlocks = 6;
+__host__ __device__ constexpr int low_block(int w, int kb) { return w < 2 ? w : 2 * (w - 1) + kb; }
+__host__ __device__ constexpr int up_block(int w, int kb) { return w < 2 ? 2 * w + kb : w + 2; }
+
+inline size_t delta_tri_elems(int planes) { return (size_t)kTriBlocks * planes * 512; }
+
+// Where a row's tokens lie: its first token row, its length, its first chunk
+// slot.  Offsets are clamped into the arrays and lengths to max_len, so that
+// wrong ones give wrong results and no access outside.
+struct DeltaRow {
+    int64_t start, len, slot0;
+};
+__device__ __forceinline__ DeltaRow delta_row(const DeltaParams& p, int b)
+{
+    DeltaRow r;
+    if (p.cu == nullptr) {
+        r.start = (int64_t)b * p.L;
+        r.len = p.L;
+        r.slot0 = (int64_t)b * p.nc;
+    } else {
+        int64_t s = p.cu[b], e = p.cu[b + 1];
+        s = s < 0 ? 0 : (s > p.L ? p.L : s);
+        e = e < s ? s : (e > p.L ? p.L : e);
+        r.start = s;
+        r.len = e - s < p.max_len ? e - s : p.max_len;
+        // floor(a + b) + 1 >= floor(a) + ceil(b): no two rows share a slot
+        r.slot0 = s / kDC + b;
+    }
+    return r;
+}
+
+// The record of row b: its index, -1 for none (a slot outside the pool), -2
+// where an earlier row names the same slot.  Called by whole workgroups; lane
+// ids run over [0, nt).
+__device__ __forceinline__ int64_t delta_record(const DeltaParams& p, int b, int tid, int nt, int* flag)
+{
+    if (p.slots == nullptr) return b;
+    const int s = p.slots[b];
+    if (s < 0 || s >= p.nslots) return -1;
+    bool seen = false;
+    for (int i = tid; i < b; i += nt) seen |= p.slots[i] == s;
+    if (tid == 0) *flag = 0;
+    __syncthreads();
+    if (seen) *flag = 1;
+    __syncthreads();
+    const int twice = *flag;
+    __syncthreads();
+    return twice ? -2 : s;
+}
+
+// x as a sum of bf16 planes.
+template <int PL> __device__ __forceinline__ void to_planes(float x, bf16 (&o)[PL])
+{
+#pragma unroll
+    for (int i = 0; i < PL; ++i) {
+        o[i] = (bf16)x;
+        x -= (float)o[i];
+    }
+}
+template <int PL> __device__ __forceinline__ void to_planes4(const f32x4& x, bf16x4 (&o)[PL])
+{
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        bf16 t[PL];
+        to_planes<PL>(x[e], t);
+#pragma unroll
+        for (int i = 0; i < PL; ++i) o[i][e] = t[i];
+    }
+}
+
+// acc += a b, both as planes; products whose planes lie LIM or more apart are
+// below what LIM planes hold.  Small ones first.
+template <int PA, int PB, int LIM>
+__device__ __forceinline__ void mma_planes(const bf16x8 (&a)[PA], const bf16x8 (&b)[PB], f32x4& acc)
+{
+#pragma unroll
+    for (int s = LIM - 1; s >= 0; --s)
+#pragma unroll
+        for (int i = 0; i < PA; ++i) {
+            const int j = s - i;
+            if (j >= 0 && j < PB) acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a[i], b[j], acc, 0, 0, 0);
+        }
+}
+
+__device__ __forceinline__ bf16x8 zero8()
+{
+    bf16x8 z;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) z[e] = (bf16)0.0f;
+    return z;
+}
+
+// 8 contiguous io values as planes; zeros where !ok (nothing is read).
+template <typename IO> struct RawRow8;
+template <> struct RawRow8<bf16> {
+    bf16x8 v;
+    __device__ __forceinline__ void load(const bf16* p, bool ok) { v = ok ? *reinterpret_cast<const bf16x8*>(p) : zero8(); }
+    __device__ __forceinline__ float get(int e) const { return (float)v[e]; }
+    __device__ __forceinline__ void planes(bf16x8 (&o)[1]) const { o[0] = v; }
+};
+template <> struct RawRow8<float> {
+    f32x4 a, b;
+    __device__ __forceinline__ void load(const float* p, bool ok)
+    {
+        const f32x4 z = {0.f, 0.f, 0.f, 0.f};
+        a = ok ? *reinterpret_cast<const f32x4*>(p) : z;
+        b = ok ? *reinterpret_cast<const f32x4*>(p + 4) : z;
+    }
+    __device__ __forceinline__ float get(int e) const { return e < 4 ? a[e & 3] : b[e & 3]; }
+    template <int PL> __device__ __forceinline__ void planes(bf16x8 (&o)[PL]) const
+    {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            bf16 t[PL];
+            to_planes<PL>(get(e), t);
+#pragma unroll
+            for (int i = 0; i < PL; ++i) o[i][e] = t[i];
+        }
+    }
+};
+
+}  // namespace m3

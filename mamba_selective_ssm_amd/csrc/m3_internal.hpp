@@ -7,6 +7,10 @@
 
 namespace m3 {
 
+// The status (m3_status) of a HIP call's result; a failure is kept for
+// m3_last_hip_error.
+int record_hip(hipError_t e);
+
 struct ScanParams;
 
 // Options of both entry points, resolved for the kernels.
