@@ -82,13 +82,19 @@ template <typename IO> struct DeltaPlanes;
 template <> struct DeltaPlanes<bf16> { static constexpr int io = 1, wide = 3, out = 2; };
 template <> struct DeltaPlanes<float> { static constexpr int io = 3, wide = 3, out = 3; };
 
-// Operand blocks of a lower triangular 64 x 64 matrix: 16 rows x 32 columns
-// each, block (w, kb) of row tile w at 0: (0,0) 1: (1,0) 2: (2,0) 3: (2,1)
-// 4: (3,0) 5: (3,1).  Of an upper triangular one (the transposes): 0: (0,0)
-// 1: (0,1) 2: (1,0) 3: (1,1) 4: (2,1) 5: (3,1).
+// Row m of 16 x 16 tile i, for the tokens of a chunk and for the rows of the
+// state alike.  A result tile leaves rows 4 g + r (r = 0..3) in lane (l, g);
+// with this order the tiles 2 kb and 2 kb + 1 leave rows 32 kb + 8 g .. + 7
+// there: the eight K values of the second operand of the next product.  So a
+// wavefront feeds a product's result to the next one in its own registers.
+__host__ __device__ constexpr int tile_row(int i, int m) { return 32 * (i >> 1) + 8 * (m >> 2) + 4 * (i & 1) + (m & 3); }
+
+// Operand blocks of a lower triangular 64 x 64 matrix, 16 rows (of tile w) x 32
+// columns each, in the order (0,0) (1,0) (2,0) (3,0) (2,1) (3,1) of (w, kb); of
+// an upper triangular one (the transposes) (0,0) (1,0) (0,1) (1,1) (2,1) (3,1).
 constexpr int kTriBlocks = 6;
-__host__ __device__ constexpr int low_block(int w, int kb) { return w < 2 ? w : 2 * (w - 1) + kb; }
-__host__ __device__ constexpr int up_block(int w, int kb) { return w < 2 ? 2 * w + kb : w + 2; }
+__host__ __device__ constexpr int low_block(int w, int kb) { return w + 2 * kb; }
+__host__ __device__ constexpr int up_block(int w, int kb) { return w + 2 * kb; }
 
 inline size_t delta_tri_elems(int planes) { return (size_t)kTriBlocks * planes * 512; }
 
@@ -136,28 +142,53 @@ __device__ __forceinline__ int64_t delta_record(const DeltaParams& p, int b, int
     return twice ? -2 : s;
 }
 
-// x as a sum of bf16 planes.
-template <int PL> __device__ __forceinline__ void to_planes(float x, bf16 (&o)[PL])
+// A bf16 pair in a scalar register.  (As a constant, (-1, 0) would become the
+// instruction's inline -1.0, which it takes for both halves.)
+__device__ __forceinline__ bf16x2 pair_of(unsigned bits)
+{
+    asm("" : "+s"(bits));
+    return __builtin_bit_cast(bf16x2, bits);
+}
+
+// Two values as sums of bf16 planes: each plane is the rounding of what the
+// ones before it left, one conversion for both.
+typedef __attribute__((__vector_size__(2 * sizeof(float)))) float f32x2;
+template <int PL> __device__ __forceinline__ void to_planes2(float x, float y, bf16x2 (&o)[PL])
 {
 #pragma unroll
     for (int i = 0; i < PL; ++i) {
-        o[i] = (bf16)x;
-        x -= (float)o[i];
+        o[i] = __builtin_convertvector(f32x2{x, y}, bf16x2);
+        if (i + 1 < PL) {
+            // x - o[0], y - o[1], one instruction each without unpacking
+            x = __builtin_amdgcn_fdot2_f32_bf16(o[i], pair_of(0x0000bf80u), x, false);
+            y = __builtin_amdgcn_fdot2_f32_bf16(o[i], pair_of(0xbf800000u), y, false);
+        }
     }
 }
 template <int PL> __device__ __forceinline__ void to_planes4(const f32x4& x, bf16x4 (&o)[PL])
 {
+    bf16x2 a[PL], b[PL];
+    to_planes2<PL>(x[0], x[1], a);
+    to_planes2<PL>(x[2], x[3], b);
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-        bf16 t[PL];
-        to_planes<PL>(x[e], t);
-#pragma unroll
-        for (int i = 0; i < PL; ++i) o[i][e] = t[i];
-    }
+    for (int i = 0; i < PL; ++i) o[i] = bf16x4{a[i][0], a[i][1], b[i][0], b[i][1]};
 }
 
-// acc += a b, both as planes; products whose planes lie LIM or more apart are
-// below what LIM planes hold.  Small ones first.
+// acc[i] += a[i] b, all as planes; products whose planes lie LIM or more apart
+// are below what LIM planes hold.  Small ones first.
+template <int T, int PA, int PB, int LIM>
+__device__ __forceinline__ void mma_tiles(const bf16x8 (&a)[T][PA], const bf16x8 (&b)[PB], f32x4* acc)
+{
+#pragma unroll
+    for (int s = LIM - 1; s >= 0; --s)
+#pragma unroll
+        for (int i = 0; i < PA; ++i) {
+            const int j = s - i;
+            if (j >= 0 && j < PB)
+#pragma unroll
+                for (int t = 0; t < T; ++t) acc[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a[t][i], b[j], acc[t], 0, 0, 0);
+        }
+}
 template <int PA, int PB, int LIM>
 __device__ __forceinline__ void mma_planes(const bf16x8 (&a)[PA], const bf16x8 (&b)[PB], f32x4& acc)
 {
@@ -168,6 +199,11 @@ __device__ __forceinline__ void mma_planes(const bf16x8 (&a)[PA], const bf16x8 (
             const int j = s - i;
             if (j >= 0 && j < PB) acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a[i], b[j], acc, 0, 0, 0);
         }
+}
+
+__device__ __forceinline__ bf16x8 join8(const bf16x4& a, const bf16x4& b)
+{
+    return __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
 }
 
 __device__ __forceinline__ bf16x8 zero8()
@@ -198,11 +234,11 @@ template <> struct RawRow8<float> {
     template <int PL> __device__ __forceinline__ void planes(bf16x8 (&o)[PL]) const
     {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            bf16 t[PL];
-            to_planes<PL>(get(e), t);
+        for (int e = 0; e < 8; e += 2) {
+            bf16x2 t[PL];
+            to_planes2<PL>(get(e), get(e + 1), t);
 #pragma unroll
-            for (int i = 0; i < PL; ++i) o[i][e] = t[i];
+            for (int i = 0; i < PL; ++i) { o[i][e] = t[i][0]; o[i][e + 1] = t[i][1]; }
         }
     }
 };

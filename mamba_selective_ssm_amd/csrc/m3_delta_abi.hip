@@ -42,8 +42,8 @@ m3_status check_sizes(int64_t batch, int64_t seqlen, int64_t H, int64_t G, int64
     if (l2norm != 0 && l2norm != 1) return M3_ERR_OPTION;
     if (l2norm && !(eps >= 0.f && eps < 3.0e38f)) return M3_ERR_OPTION;
     if (!(fabsf(scale) < 3.0e38f)) return M3_ERR_OPTION;
-    // a row's offsets of one chunk and a record's are kept in 32 bits
-    if (H > ((int64_t)1 << 20) || batch > ((int64_t)1 << 24)) return M3_ERR_UNSUPPORTED;
+    // offsets inside one chunk are kept in 32 bits: 64 H 128 values
+    if (H > ((int64_t)1 << 14) || batch > ((int64_t)1 << 24)) return M3_ERR_UNSUPPORTED;
     if (batch * H > ((int64_t)1 << 24)) return M3_ERR_UNSUPPORTED;
     return M3_OK;
 }

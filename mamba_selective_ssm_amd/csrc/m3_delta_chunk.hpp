@@ -1,583 +1,350 @@
-// Gated delta rule: the kernel that makes what a chunk's products need and
-// no state enters (T, A, per-token factors), and the walk over the chunks.
+// Gated delta rule: the kernel that makes what a chunk's products need and no
+// state enters: T, A and per-token factors.
 #pragma once
 
 #include "m3_delta.hpp"
 
 namespace m3 {
 
-// acc += A B for 16 x 16 float32 tiles in LDS (row-major, leading dimensions
-// lda, ldb): lane (l, g) supplies A[l][k], B[k][l] of k = 4 kk + g.
-__device__ __forceinline__ void tile_mm(const float* A, int lda, const float* B, int ldb, int l, int g, f32x4& acc)
+// acc += A B for 16 x 16 float32 tiles in LDS (row-major, leading dimension
+// LD): lane (l, g) supplies A[l][k], B[k][l] of k = 4 kk + g.
+template <int LD>
+__device__ __forceinline__ void tile_mm(const float* A, const float* B, int l, int g, f32x4& acc)
 {
 #pragma unroll
     for (int kk = 0; kk < 4; ++kk)
-        acc = __builtin_amdgcn_mfma_f32_16x16x4f32(A[l * lda + 4 * kk + g], B[(4 * kk + g) * ldb + l], acc, 0, 0, 0);
+        acc = __builtin_amdgcn_mfma_f32_16x16x4f32(A[l * LD + 4 * kk + g], B[(4 * kk + g) * LD + l], acc, 0, 0, 0);
 }
-__device__ __forceinline__ void tile_put(float* C, int ldc, int l, int g, const f32x4& v)
+template <int LD>
+__device__ __forceinline__ void tile_put(float* C, int l, int g, const f32x4& v)
 {
 #pragma unroll
-    for (int r = 0; r < 4; ++r) C[(4 * g + r) * ldc + l] = v[r];
+    for (int r = 0; r < 4; ++r) C[(4 * g + r) * LD + l] = v[r];
+}
+
+// What a wavefront's lanes have written to LDS before is there for all its
+// lanes after: its LDS instructions run in order, so only the compiler's order
+// has to be held.
+__device__ __forceinline__ void wave_order()
+{
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+}
+
+// Inclusive prefix sum across a wavefront in float64, by the lane moves of
+// wave_inclusive_sum on both halves.
+template <int CTRL, int ROW_MASK> __device__ __forceinline__ double dpp_moved_d(double x)
+{
+    const long long b = __builtin_bit_cast(long long, x);
+    const unsigned lo = (unsigned)dpp_moved_i<CTRL, ROW_MASK>((int)(b & 0xffffffffll));
+    const unsigned hi = (unsigned)dpp_moved_i<CTRL, ROW_MASK>((int)(b >> 32));
+    return __builtin_bit_cast(double, (long long)(((unsigned long long)hi << 32) | lo));
+}
+__device__ __forceinline__ double wave_inclusive_sum_d(double v)
+{
+    v += dpp_moved_d<0x111, 0xf>(v);
+    v += dpp_moved_d<0x112, 0xf>(v);
+    v += dpp_moved_d<0x114, 0xf>(v);
+    v += dpp_moved_d<0x118, 0xf>(v);
+    v += dpp_moved_d<0x142, 0xa>(v);
+    v += dpp_moved_d<0x143, 0xc>(v);
+    return v;
+}
+
+// 16 x 32 operand block (w, kb) of a triangular matrix in LDS as planes: rows
+// tile_row(w, l), columns 32 kb + 8 g ..+7 (TR: of its transpose), zero outside
+// the triangle.
+template <int PL, int LD, bool TR>
+__device__ __forceinline__ void put_block(bf16* dst, const float* M, int w, int kb, int l, int g, int lane)
+{
+    const int row = tile_row(w, l), c0 = 32 * kb;
+    float x[8];
+    if constexpr (TR) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) x[e] = M[(c0 + 8 * g + e) * LD + row];
+    } else {
+        const f32x4 a = *reinterpret_cast<const f32x4*>(M + row * LD + c0 + 8 * g);
+        const f32x4 b = *reinterpret_cast<const f32x4*>(M + row * LD + c0 + 8 * g + 4);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) { x[e] = a[e]; x[4 + e] = b[e]; }
+    }
+    bf16x8 o[PL];
+#pragma unroll
+    for (int e = 0; e < 8; e += 2) {
+        const int col = c0 + 8 * g + e;
+        const float x0 = (TR ? col >= row : col <= row) ? x[e] : 0.f;
+        const float x1 = (TR ? col + 1 >= row : col + 1 <= row) ? x[e + 1] : 0.f;
+        bf16x2 t[PL];
+        to_planes2<PL>(x0, x1, t);
+#pragma unroll
+        for (int i = 0; i < PL; ++i) { o[i][e] = t[i][0]; o[i][e + 1] = t[i][1]; }
+    }
+#pragma unroll
+    for (int i = 0; i < PL; ++i) *reinterpret_cast<bf16x8*>(dst + i * 512 + lane * 8) = o[i];
+}
+template <int PL, int LD> __device__ __forceinline__ void put_lower(bf16* dst, const float* M, int l, int g, int lane)
+{
+#pragma unroll
+    for (int w = 0; w < 4; ++w)
+#pragma unroll
+        for (int kb = 0; kb <= w / 2; ++kb) put_block<PL, LD, false>(dst + low_block(w, kb) * PL * 512, M, w, kb, l, g, lane);
+}
+template <int PL, int LD> __device__ __forceinline__ void put_upper(bf16* dst, const float* M, int l, int g, int lane)
+{
+#pragma unroll
+    for (int w = 0; w < 4; ++w)
+#pragma unroll
+        for (int kb = w / 2; kb < 2; ++kb) put_block<PL, LD, true>(dst + up_block(w, kb) * PL * 512, M, w, kb, l, g, lane);
 }
 
 // What one chunk of one head needs besides its rows:
 //   T = (I + M)^-1, A = scale D o Q K^T (rows divided by their norms where the
 //   call asks for it), and per token  beta | beta e^G / |k| | e^(G_last - G) /
 //   |k| | scale e^G / |q|, then e^G_last.
-// One workgroup of four waves per chunk and head, wave w on rows 16w..16w+15.
-// K and Q rows are the operands as they lie in memory (lane: one row, 8
-// columns), so the two 64 x 64 products take no LDS.  M is inverted by blocks:
-// substitution inside the four 16 x 16 diagonal blocks (one column per lane,
-// in registers), then pairs of blocks joined, [[A,0],[C,B]]^-1 = [[A^-1,0],
-// [-B^-1 C A^-1, B^-1]], with float32 matrix instructions.  Substitution and
-// not the product (I-M)(I+M^2)(I+M^4).., whose terms cancel where keys repeat.
-// G is summed in 64 bits and kept as two float32 in units of log 2: the
-// difference of two sums keeps float32's relative precision after a token
-// whose decay is near zero.
+// One wavefront per chunk and head, on its own: no barriers, and the steps
+// that wait on each other (the sums over the chunk, the inverse) run beside
+// those of the other wavefronts on the SIMD.  K and Q rows are the operands as
+// they lie in memory (lane: one row, 8 columns), so the two 64 x 64 products
+// take no LDS.  M is inverted by blocks, in place: substitution inside the
+// four 16 x 16 diagonal blocks (lane (l, g): column l of block g, in
+// registers), then pairs of blocks joined, [[A,0],[C,B]]^-1 = [[A^-1,0],
+// [-B^-1 C A^-1, B^-1]], with float32 matrix instructions; C A^-1 waits in the
+// unused block above the diagonal.  Substitution and not the product
+// (I-M)(I+M^2)(I+M^4).., whose terms cancel where keys repeat.  G is summed in
+// 64 bits and kept as two float32 in units of log 2: the difference of two
+// sums keeps float32's relative precision after a token whose decay is near
+// zero.  Rows past the end read the last row again; their beta is 0 and their
+// g is 0, which makes their rows of T the identity's.
 template <typename IO, int N, bool BWD>
-__global__ __launch_bounds__(256) void delta_chunk_kernel(const DeltaParams p, bf16* ttf, bf16* atf)
+__global__ __launch_bounds__(64) void delta_chunk_kernel(const DeltaParams p, bf16* ttf, bf16* atf)
 {
     constexpr int KP = DeltaPlanes<IO>::io, WP = DeltaPlanes<IO>::wide, OP = DeltaPlanes<IO>::out;
     constexpr int AP = BWD ? WP : OP;     // the gradient's path is float32 throughout
     constexpr int KB = N / 32, LD = 68;
-    __shared__ float sGh[64], sGl[64], sBeta[64], sRk[64], sRq[64], sE[64], sD[64];
     __shared__ __attribute__((aligned(16))) float sM[64 * LD];
-    __shared__ __attribute__((aligned(16))) float sT[64 * LD];   // A first, then T
-    __shared__ float sX[32 * 36];
+    __shared__ __attribute__((aligned(16))) float sGh[64], sGl[64], sBk[64], sRk[64], sRq[64];
 
-    const int tid = threadIdx.x, lane = tid & 63, l = lane & 15, g = lane >> 4;
-    const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int lane = threadIdx.x, l = lane & 15, g = lane >> 4;
     const int64_t bid = blockIdx.x;
     const int h = (int)(bid % p.H);
-    const int64_t bc = bid / p.H;
-    const int c = (int)(bc % p.nc), b = (int)(bc / p.nc);
+    const int bc = (int)(bid / p.H);
+    const int c = bc % p.nc, b = bc / p.nc;
     const DeltaRow row = delta_row(p, b);
     if ((int64_t)c * kDC >= row.len) return;
     const int64_t t0 = row.start + (int64_t)c * kDC;
     const int nv = row.len - (int64_t)c * kDC < kDC ? (int)(row.len - (int64_t)c * kDC) : kDC;
     const int64_t ci = (row.slot0 + c) * p.H + h;
     const int hg = h / (p.H / p.G);
-    const IO* kb_ = reinterpret_cast<const IO*>(p.k) + (t0 * p.G + hg) * N;
-    const IO* qb_ = reinterpret_cast<const IO*>(p.q) + (t0 * p.G + hg) * N;
-    const int64_t rs = (int64_t)p.G * N;   // row stride of q and k
+    const IO* kp = reinterpret_cast<const IO*>(p.k) + (t0 * p.G + hg) * N;
+    const IO* qp = reinterpret_cast<const IO*>(p.q) + (t0 * p.G + hg) * N;
+    const int rs = p.G * N;   // row stride of q and k
 
-    // this wave's rows of K and Q
-    RawRow8<IO> kr[KB], qr[KB];
-    const int irow = 16 * w + l;
+    const int tok = lane < nv ? lane : nv - 1;
+    float gv = p.g[(t0 + tok) * p.H + h];
+    float bv = p.beta[(t0 + tok) * p.H + h];
+    RawRow8<IO> kr[4][KB], qr[KB];
+    int off[4];
 #pragma unroll
-    for (int kb = 0; kb < KB; ++kb) {
-        kr[kb].load(kb_ + irow * rs + 32 * kb + 8 * g, irow < nv);
-        qr[kb].load(qb_ + irow * rs + 32 * kb + 8 * g, irow < nv);
+    for (int rt = 0; rt < 4; ++rt) {
+        const int i = 16 * rt + l < nv ? 16 * rt + l : nv - 1;
+        off[rt] = i * rs + 8 * g;
+#pragma unroll
+        for (int kb = 0; kb < KB; ++kb) kr[rt][kb].load(kp + off[rt] + 32 * kb, true);
     }
+#pragma unroll
+    for (int kb = 0; kb < KB; ++kb) qr[kb].load(qp + off[0] + 32 * kb, true);
 
-    if (w == 0) {
-        const bool ok = lane < nv;
-        float gv = ok ? p.g[(t0 + lane) * p.H + h] : 0.f;
-        const float bv = ok ? p.beta[(t0 + lane) * p.H + h] : 0.f;
-        gv = gv < -1024.f ? -1024.f : gv;   // exp is zero there; keeps -inf out of differences
-        double s = (double)gv * 1.4426950408889634;
-#pragma unroll
-        for (int o = 1; o < 64; o <<= 1) {
-            const double t = __shfl_up(s, o);
-            if (lane >= o) s += t;
-        }
-        const double last = __shfl(s, 63);
-        sGh[lane] = (float)s;
-        sGl[lane] = (float)(s - (double)(float)s);
-        sBeta[lane] = bv;
-        sE[lane] = exp2f((float)s);
-        sD[lane] = exp2f((float)(last - s));
-        if (!p.l2norm) {
-            sRk[lane] = 1.f;
-            sRq[lane] = 1.f;
-        }
-    }
+    const bool real = lane < nv;
+    gv = real ? (gv < -1024.f ? -1024.f : gv) : 0.f;   // exp is zero there; keeps -inf out of differences
+    bv = real ? bv : 0.f;
+    const double G = wave_inclusive_sum_d((double)gv * 1.4426950408889634);
+    const double Gl = __shfl(G, 63);
+    const float gh = (float)G;
+    const float eG = __builtin_amdgcn_exp2f(gh), dG = __builtin_amdgcn_exp2f((float)(Gl - G));
+    sGh[lane] = gh;
+    sGl[lane] = (float)(G - (double)gh);
 
-    // K K^T and Q K^T, column tiles 0..w
-    f32x4 kk[4], qk[4];
-    const f32x4 fz = {0.f, 0.f, 0.f, 0.f};
-    for (int ct = 0; ct < 4; ++ct) {
-        kk[ct] = fz;
-        qk[ct] = fz;
-    }
-    float q2 = 0.f;
-    if (p.l2norm) {
+    // K K^T, tiles on and below the diagonal
+    f32x4 kk[4][4];
 #pragma unroll
-        for (int kb = 0; kb < KB; ++kb)
+    for (int rt = 0; rt < 4; ++rt)
 #pragma unroll
-            for (int e = 0; e < 8; ++e) q2 += qr[kb].get(e) * qr[kb].get(e);
-        q2 += __shfl_xor(q2, 16);
-        q2 += __shfl_xor(q2, 32);
-        if (g == 0) sRq[irow] = irow < nv ? 1.f / sqrtf(q2 + p.eps) : 0.f;
-    }
+        for (int ct = 0; ct <= rt; ++ct) kk[rt][ct] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-    for (int ct = 0; ct < 4; ++ct) {
-        if (ct > w) continue;   // wave-uniform
-        const int jrow = 16 * ct + l;
-#pragma unroll
-        for (int kb = 0; kb < KB; ++kb) {
-            RawRow8<IO> jr;
-            jr.load(kb_ + jrow * rs + 32 * kb + 8 * g, jrow < nv);
-            bf16x8 a[KP], qa[KP], j[KP];
-            kr[kb].planes(a);
-            qr[kb].planes(qa);
-            jr.planes(j);
-            mma_planes<KP, KP, WP>(a, j, kk[ct]);
-            mma_planes<KP, KP, WP>(qa, j, qk[ct]);
-        }
-    }
-    if (p.l2norm) {
+    for (int kb = 0; kb < KB; ++kb)
 #pragma unroll
         for (int ct = 0; ct < 4; ++ct) {
-            if (ct != w) continue;
+            bf16x8 j[KP];
+            kr[ct][kb].planes(j);
+#pragma unroll
+            for (int rt = ct; rt < 4; ++rt) {
+                bf16x8 a[KP];
+                kr[rt][kb].planes(a);
+                mma_planes<KP, KP, WP>(a, j, kk[rt][ct]);
+            }
+        }
+    float rk = 1.f, rq = 1.f;
+    if (p.l2norm) {
+#pragma unroll
+        for (int rt = 0; rt < 4; ++rt)
 #pragma unroll
             for (int r = 0; r < 4; ++r)
-                if (l == 4 * g + r) {   // the diagonal: |k|^2
-                    const int i = 16 * w + l;
-                    sRk[i] = i < nv ? 1.f / sqrtf(kk[ct][r] + p.eps) : 0.f;
-                }
-        }
+                if (l == 4 * g + r) sRk[16 * rt + l] = 1.f / sqrtf(kk[rt][rt][r] + p.eps);   // the diagonal: |k|^2
+        wave_order();
+        rk = sRk[lane];
+    } else {
+        sRk[lane] = 1.f;
     }
-    __syncthreads();
+    sBk[lane] = bv * rk;
+    wave_order();
 
-    // M and A; entries above the diagonal stay out
+    // A = scale D o Q K^T, one row tile at a time
+    const f32x4 fz = {0.f, 0.f, 0.f, 0.f};
+    float cgh[4], cgl[4], crk[4];
 #pragma unroll
     for (int ct = 0; ct < 4; ++ct) {
-        if (ct > w) continue;
-        const int j = 16 * ct + l;
-        const float gh = sGh[j], gl = sGl[j], rkj = sRk[j];
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-            const int i = 16 * w + 4 * g + r;
-            const float D = exp2f((sGh[i] - gh) + (sGl[i] - gl)) * rkj;
-            sM[i * LD + j] = j < i ? sBeta[i] * sRk[i] * D * kk[ct][r] : 0.f;
-            sT[i * LD + j] = j <= i ? p.scale * sRq[i] * D * qk[ct][r] : 0.f;
-        }
+        cgh[ct] = sGh[16 * ct + l];
+        cgl[ct] = sGl[16 * ct + l];
+        crk[ct] = sRk[16 * ct + l];
     }
-    if (w == 0) {   // per-token factors
+#pragma unroll
+    for (int rt = 0; rt < 4; ++rt) {
+        f32x4 qk[4] = {fz, fz, fz, fz};
+        float q2 = 0.f;
+#pragma unroll
+        for (int kb = 0; kb < KB; ++kb) {
+            bf16x8 a[KP];
+            qr[kb].planes(a);
+            if (p.l2norm)
+#pragma unroll
+                for (int e = 0; e < 8; ++e) q2 += qr[kb].get(e) * qr[kb].get(e);
+#pragma unroll
+            for (int ct = 0; ct <= rt; ++ct) {
+                bf16x8 j[KP];
+                kr[ct][kb].planes(j);
+                mma_planes<KP, KP, WP>(a, j, qk[ct]);
+            }
+            if (rt < 3) qr[kb].load(qp + off[rt < 3 ? rt + 1 : 3] + 32 * kb, true);
+        }
+        if (p.l2norm) {
+            q2 += __shfl_xor(q2, 16);
+            q2 += __shfl_xor(q2, 32);
+            q2 = 1.f / sqrtf(q2 + p.eps);
+        } else {
+            q2 = 1.f;
+        }
+        if (g == 0) sRq[16 * rt + l] = q2;
+        wave_order();
+        const f32x4 gh4 = *reinterpret_cast<const f32x4*>(&sGh[16 * rt + 4 * g]);
+        const f32x4 gl4 = *reinterpret_cast<const f32x4*>(&sGl[16 * rt + 4 * g]);
+        const f32x4 rq4 = *reinterpret_cast<const f32x4*>(&sRq[16 * rt + 4 * g]);
+        const f32x4 bk4 = *reinterpret_cast<const f32x4*>(&sBk[16 * rt + 4 * g]);
+#pragma unroll
+        for (int ct = 0; ct <= rt; ++ct)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                const bool diag = ct == rt;
+                const int i = 4 * g + r;   // row in the tile
+                float D = __builtin_amdgcn_exp2f((gh4[r] - cgh[ct]) + (gl4[r] - cgl[ct])) * crk[ct];
+                if (diag && l > i) D = 0.f;
+                sM[(16 * rt + i) * LD + 16 * ct + l] = p.scale * rq4[r] * D * qk[ct][r];
+                // D's last use is M: kk becomes M here
+                kk[rt][ct][r] = (diag && l >= i) ? 0.f : bk4[r] * D * kk[rt][ct][r];
+            }
+    }
+    wave_order();
+    rq = sRq[lane];
+    {
         float* sc = p.sc + ci * (kDScal * 64);
-        const float rk = sRk[lane], e = sE[lane], bv = sBeta[lane];
         sc[lane] = bv;
-        sc[64 + lane] = bv * e * rk;
-        sc[128 + lane] = sD[lane] * rk;
-        sc[192 + lane] = p.scale * e * sRq[lane];
-        if (lane == 0) sc[256] = sE[63];
+        sc[64 + lane] = bv * eG * rk;
+        sc[128 + lane] = dG * rk;
+        sc[192 + lane] = p.scale * eG * rq;
+        sc[256 + lane] = __builtin_amdgcn_exp2f((float)Gl);   // e^G_last, for every lane
         if (BWD) sc[320 + lane] = rk;
     }
-    __syncthreads();
+    if (!BWD)
+        put_lower<AP, LD>(p.af + ci * (kTriBlocks * AP * 512), sM, l, g, lane);
+    else
+        put_upper<AP, LD>(atf + ci * (kTriBlocks * AP * 512), sM, l, g, lane);
 
-    // A in operand order: the wave's own rows
+    // M takes A's place
+    wave_order();
 #pragma unroll
-    for (int kb = 0; kb < 2; ++kb) {
-        if (kb > (w >> 1)) continue;
-        bf16x8 o[AP];
+    for (int rt = 0; rt < 4; ++rt)
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            const int col = 32 * kb + 8 * g + e;
-            bf16 t[AP];
-            to_planes<AP>(col <= irow ? sT[irow * LD + col] : 0.f, t);
-#pragma unroll
-            for (int i = 0; i < AP; ++i) o[i][e] = t[i];
-        }
-        if (!BWD)
-#pragma unroll
-            for (int i = 0; i < AP; ++i)
-                *reinterpret_cast<bf16x8*>(p.af + ci * (kTriBlocks * AP * 512) + ((low_block(w, kb) * AP + i) * 64 + lane) * 8) = o[i];
-    }
-    if (BWD) {   // A^T: row j of the transpose is column j
-#pragma unroll
-        for (int kb = 0; kb < 2; ++kb) {
-            if (kb < (w >> 1)) continue;
-            bf16x8 o[AP];
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                const int col = 32 * kb + 8 * g + e;
-                bf16 t[AP];
-                to_planes<AP>(col >= irow ? sT[col * LD + irow] : 0.f, t);
-#pragma unroll
-                for (int i = 0; i < AP; ++i) o[i][e] = t[i];
-            }
-#pragma unroll
-            for (int i = 0; i < AP; ++i)
-                *reinterpret_cast<bf16x8*>(atf + ci * (kTriBlocks * AP * 512) + ((up_block(w, kb) * AP + i) * 64 + lane) * 8) = o[i];
-        }
-    }
-    __syncthreads();   // sT is T from here
-
-    // diagonal block of rows 16w: column l of its inverse
+        for (int ct = 0; ct <= rt; ++ct) tile_put<LD>(&sM[16 * rt * LD + 16 * ct], l, g, kk[rt][ct]);
+    wave_order();
+    // the diagonal blocks: column l of block g
     {
+        const float* m0 = &sM[16 * g * LD + 16 * g];
         float x[16];
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
             float s = i == l ? 1.f : 0.f;
 #pragma unroll
             for (int j4 = 0; j4 < (i + 3) / 4; ++j4) {
-                const f32x4 m = *reinterpret_cast<const f32x4*>(&sM[(16 * w + i) * LD + 16 * w + 4 * j4]);
+                const f32x4 m = *reinterpret_cast<const f32x4*>(m0 + i * LD + 4 * j4);
 #pragma unroll
                 for (int e = 0; e < 4; ++e)
                     if (4 * j4 + e < i) s -= m[e] * x[4 * j4 + e];
             }
             x[i] = s;
         }
-        if (g == 0) {
+        wave_order();
 #pragma unroll
-            for (int i = 0; i < 16; ++i) sT[(16 * w + i) * LD + 16 * w + l] = x[i];
-        }
+        for (int i = 0; i < 16; ++i) sM[(16 * g + i) * LD + 16 * g + l] = x[i];
     }
-    __syncthreads();
+    wave_order();
     // blocks (1,0) and (3,2)
-    if (w < 2) {
-        f32x4 x = fz;
-        tile_mm(&sM[(32 * w + 16) * LD + 32 * w], LD, &sT[32 * w * LD + 32 * w], LD, l, g, x);
-        tile_put(sX + w * 320, 20, l, g, x);
+    {
+        f32x4 x[2] = {fz, fz};
+#pragma unroll
+        for (int w = 0; w < 2; ++w) tile_mm<LD>(&sM[(32 * w + 16) * LD + 32 * w], &sM[32 * w * LD + 32 * w], l, g, x[w]);
+#pragma unroll
+        for (int w = 0; w < 2; ++w) tile_put<LD>(&sM[32 * w * LD + 32 * w + 16], l, g, x[w]);
+        wave_order();
+#pragma unroll
+        for (int w = 0; w < 2; ++w) {
+            x[w] = fz;
+            tile_mm<LD>(&sM[(32 * w + 16) * LD + 32 * w + 16], &sM[32 * w * LD + 32 * w + 16], l, g, x[w]);
+        }
+#pragma unroll
+        for (int w = 0; w < 2; ++w) tile_put<LD>(&sM[(32 * w + 16) * LD + 32 * w], l, g, -x[w]);
     }
-    __syncthreads();
-    if (w < 2) {
-        f32x4 x = fz;
-        tile_mm(&sT[(32 * w + 16) * LD + 32 * w + 16], LD, sX + w * 320, 20, l, g, x);
-        tile_put(&sT[(32 * w + 16) * LD + 32 * w], LD, l, g, -x);
-    }
-    __syncthreads();
+    wave_order();
     // the 32 x 32 block below: X = C A^-1, then -B^-1 X
     {
-        const int ta = w >> 1, tb = w & 1;
-        f32x4 x = fz;
-        for (int k = tb; k < 2; ++k)
-            tile_mm(&sM[(32 + 16 * ta) * LD + 16 * k], LD, &sT[16 * k * LD + 16 * tb], LD, l, g, x);
-        tile_put(sX + 16 * ta * 36 + 16 * tb, 36, l, g, x);
-        __syncthreads();
-        x = fz;
-        for (int k = 0; k <= ta; ++k)
-            tile_mm(&sT[(32 + 16 * ta) * LD + 32 + 16 * k], LD, sX + 16 * k * 36 + 16 * tb, 36, l, g, x);
-        tile_put(&sT[(32 + 16 * ta) * LD + 16 * tb], LD, l, g, -x);
-    }
-    __syncthreads();
-
-    // T in operand order
+        f32x4 x[2][2] = {{fz, fz}, {fz, fz}};
 #pragma unroll
-    for (int kb = 0; kb < 2; ++kb) {
-        if (kb > (w >> 1)) continue;
-        bf16x8 o[WP];
+        for (int ta = 0; ta < 2; ++ta)
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            const int col = 32 * kb + 8 * g + e;
-            bf16 t[WP];
-            to_planes<WP>(col <= irow ? sT[irow * LD + col] : 0.f, t);
+            for (int tb = 0; tb < 2; ++tb)
 #pragma unroll
-            for (int i = 0; i < WP; ++i) o[i][e] = t[i];
-        }
+                for (int k = tb; k < 2; ++k)
+                    tile_mm<LD>(&sM[(32 + 16 * ta) * LD + 16 * k], &sM[16 * k * LD + 16 * tb], l, g, x[ta][tb]);
 #pragma unroll
-        for (int i = 0; i < WP; ++i)
-            *reinterpret_cast<bf16x8*>(p.tf + ci * (kTriBlocks * WP * 512) + ((low_block(w, kb) * WP + i) * 64 + lane) * 8) = o[i];
-    }
-    if (BWD) {
+        for (int ta = 0; ta < 2; ++ta)
 #pragma unroll
-        for (int kb = 0; kb < 2; ++kb) {
-            if (kb < (w >> 1)) continue;
-            bf16x8 o[WP];
+            for (int tb = 0; tb < 2; ++tb) tile_put<LD>(&sM[16 * ta * LD + 32 + 16 * tb], l, g, x[ta][tb]);
+        wave_order();
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                const int col = 32 * kb + 8 * g + e;
-                bf16 t[WP];
-                to_planes<WP>(col >= irow ? sT[col * LD + irow] : 0.f, t);
+        for (int ta = 0; ta < 2; ++ta)
 #pragma unroll
-                for (int i = 0; i < WP; ++i) o[i][e] = t[i];
+            for (int tb = 0; tb < 2; ++tb) {
+                x[ta][tb] = fz;
+#pragma unroll
+                for (int k = 0; k <= ta; ++k)
+                    tile_mm<LD>(&sM[(32 + 16 * ta) * LD + 32 + 16 * k], &sM[16 * k * LD + 32 + 16 * tb], l, g, x[ta][tb]);
             }
 #pragma unroll
-            for (int i = 0; i < WP; ++i)
-                *reinterpret_cast<bf16x8*>(ttf + ci * (kTriBlocks * WP * 512) + ((up_block(w, kb) * WP + i) * 64 + lane) * 8) = o[i];
-        }
+        for (int ta = 0; ta < 2; ++ta)
+#pragma unroll
+            for (int tb = 0; tb < 2; ++tb) tile_put<LD>(&sM[(32 + 16 * ta) * LD + 16 * tb], l, g, -x[ta][tb]);
     }
-}
-
-// LDS of the walk, in bf16 elements.
-template <typename IO, int N, int NCG> struct WalkLds {
-    static constexpr int KP = DeltaPlanes<IO>::io, WP = DeltaPlanes<IO>::wide, OP = DeltaPlanes<IO>::out;
-    static constexpr int LK = N + 8, LT = 72, C = 16 * NCG;
-    static constexpr int k = 0, s = k + KP * 64 * LK, r = s + WP * C * LK, u2 = r + WP * C * LT, u = u2 + WP * C * LT,
-                         total = u + OP * C * LT;
-    static constexpr size_t bytes = 2 * (size_t)total;
-};
-
-// The walk over one row's chunks for one head and 16 NCG columns of V.
-//
-// Per chunk, wave w of a column group of 16 holds rows 16w..16w+15 of the
-// chunk and rows n of the state in tiles w, w + 4:
-//   P = K S, Q S        (operands: its K and Q rows from memory, S from LDS)
-//   U = T (beta V - sp P)
-//   S = e^G_last S + K^T (d U),  O = e Q S + A U
-// three stages with a barrier after each, because the next stage's second
-// operand is what all four waves have just made.  Everything that does not
-// depend on the state (rows, T, A, factors) is read straight into operand
-// registers one chunk ahead.  The walk's time is the latency of this chain,
-// not its arithmetic, so a call with few (row, head) pairs takes 16 columns per
-// workgroup and spreads over the chip.
-// TRAIN: writes each chunk's first state and U for the gradient instead of O.
-template <typename IO, int N, int NCG, bool TRAIN>
-__global__ __launch_bounds__(256 * NCG) void delta_walk_kernel(const DeltaParams p, float* Sbuf, float* Ubuf)
-{
-    using Ld = WalkLds<IO, N, NCG>;
-    constexpr int KP = Ld::KP, WP = Ld::WP, OP = Ld::OP, LK = Ld::LK, LT = Ld::LT, C = Ld::C;
-    constexpr int KB = N / 32, NT = N / 16, TI = (NT + 3) / 4;
-    extern __shared__ __attribute__((aligned(16))) bf16 dlds[];
-    __shared__ int sflag;
-    bf16 *sK = dlds + Ld::k, *sS = dlds + Ld::s, *sR = dlds + Ld::r, *sU2 = dlds + Ld::u2, *sU = dlds + Ld::u;
-
-    const int tid = threadIdx.x, lane = tid & 63, l = lane & 15, g = lane >> 4;
-    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int w = wave & 3, cg = wave >> 2;
-    // the slices of one (row, head) run on one XCD and share its L2
-    const int nsl = p.P / C;
-    const int64_t idx = blockIdx.x >> 3;
-    const int64_t unit = (idx / nsl) * 8 + (blockIdx.x & 7);
-    if (unit >= (int64_t)p.rows * p.H) return;
-    int64_t b64, h64;
-    split_bh(unit, p.H, b64, h64);
-    const int b = (int)b64, h = (int)h64;
-    const int p0 = (int)(idx % nsl) * C + cg * 16;   // this wave's first column
-    const DeltaRow row = delta_row(p, b);
-    const int64_t rec = TRAIN ? b : delta_record(p, b, tid, 256 * NCG, &sflag);
-    const int nch = (int)((row.len + kDC - 1) / kDC);
-    const int hg = h / (p.H / p.G);
-    const int64_t rs = (int64_t)p.G * N, vs = (int64_t)p.H * p.P;
-    const IO* kp = reinterpret_cast<const IO*>(p.k) + (row.start * p.G + hg) * N;
-    const IO* qp = reinterpret_cast<const IO*>(p.q) + (row.start * p.G + hg) * N;
-    const IO* vp = reinterpret_cast<const IO*>(p.v) + (row.start * p.H + h) * p.P + p0 + l;
-    IO* op = reinterpret_cast<IO*>(p.o) + (row.start * p.H + h) * p.P + p0 + l;
-
-    // state tiles: rows 16 (w + 4 i) + 4 g + r, column l
-    f32x4 S[TI];
-#pragma unroll
-    for (int i = 0; i < TI; ++i) {
-        const int n0 = 16 * (w + 4 * i) + 4 * g;
-        const bool mine = w + 4 * i < NT;
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-            S[i][r] = mine && p.h_in != nullptr && rec >= 0
-                          ? p.h_in[((rec * p.H + h) * N + n0 + r) * p.P + p0 + l] : 0.f;
-            if (rec == -2) S[i][r] = __builtin_nanf("");   // the record belongs to an earlier row
-        }
-    }
-    auto put_state = [&]() {
-#pragma unroll
-        for (int i = 0; i < TI; ++i) {
-            if (w + 4 * i >= NT) continue;
-            bf16x4 o[WP];
-            to_planes4<WP>(S[i], o);
-#pragma unroll
-            for (int j = 0; j < WP; ++j)
-                *reinterpret_cast<bf16x4*>(sS + (j * C + cg * 16 + l) * LK + 16 * (w + 4 * i) + 4 * g) = o[j];
-        }
-    };
-    put_state();
-
-    const int irow = 16 * w + l;          // operand row of this lane
-    const int drow = 16 * w + 4 * g;      // first result row of this lane
-    RawRow8<IO> kr[KB], qr[KB];
-    bf16x8 tf[2][WP], af[2][OP];
-    float v[4];
-    f32x4 fb, fp, fu, fo;
-    float eL;
-    const int nb = (w >> 1) + 1;          // 32-column blocks of this wave's rows in T and A
-    auto load_k = [&](int c) {
-        const int64_t t = (int64_t)c * kDC + irow;
-#pragma unroll
-        for (int kb = 0; kb < KB; ++kb) kr[kb].load(kp + t * rs + 32 * kb + 8 * g, t < row.len);
-    };
-    auto load_q = [&](int c) {
-        const int64_t t = (int64_t)c * kDC + irow;
-#pragma unroll
-        for (int kb = 0; kb < KB; ++kb) qr[kb].load(qp + t * rs + 32 * kb + 8 * g, t < row.len);
-    };
-    auto load_v = [&](int c) {
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-            const int64_t t = (int64_t)c * kDC + drow + r;
-            v[r] = t < row.len ? to_f32(vp[t * vs]) : 0.f;
-        }
-    };
-    auto load_t = [&](int c) {
-        const bf16* src = p.tf + ((row.slot0 + c) * p.H + h) * (kTriBlocks * WP * 512) + lane * 8;
-#pragma unroll
-        for (int kb = 0; kb < 2; ++kb)
-            if (kb < nb)
-#pragma unroll
-                for (int i = 0; i < WP; ++i)
-                    tf[kb][i] = *reinterpret_cast<const bf16x8*>(src + (low_block(w, kb) * WP + i) * 512);
-    };
-    auto load_a = [&](int c) {
-        const bf16* src = p.af + ((row.slot0 + c) * p.H + h) * (kTriBlocks * OP * 512) + lane * 8;
-#pragma unroll
-        for (int kb = 0; kb < 2; ++kb)
-            if (kb < nb)
-#pragma unroll
-                for (int i = 0; i < OP; ++i)
-                    af[kb][i] = *reinterpret_cast<const bf16x8*>(src + (low_block(w, kb) * OP + i) * 512);
-    };
-    auto load_f = [&](int c) {
-        const float* src = p.sc + ((row.slot0 + c) * p.H + h) * (kDScal * 64);
-        fb = *reinterpret_cast<const f32x4*>(src + drow);
-        fp = *reinterpret_cast<const f32x4*>(src + 64 + drow);
-        fu = *reinterpret_cast<const f32x4*>(src + 128 + drow);
-        fo = *reinterpret_cast<const f32x4*>(src + 192 + drow);
-        eL = src[256];
-    };
-    if (nch > 0) {
-        load_k(0);
-        if (!TRAIN) load_q(0);
-        load_v(0);
-        load_f(0);
-        load_t(0);
-        if (!TRAIN) load_a(0);
-    }
-    __syncthreads();
-
-    for (int c = 0; c < nch; ++c) {
-        const int64_t ci = (row.slot0 + c) * p.H + h;
-        if (TRAIN) {
-#pragma unroll
-            for (int i = 0; i < TI; ++i)
-                if (w + 4 * i < NT)
-#pragma unroll
-                    for (int r = 0; r < 4; ++r)
-                        Sbuf[(ci * N + 16 * (w + 4 * i) + 4 * g + r) * p.P + p0 + l] = S[i][r];
-        }
-        // stage 1
-        f32x4 aP = {0.f, 0.f, 0.f, 0.f}, aQ = aP;
-#pragma unroll
-        for (int kb = 0; kb < KB; ++kb) {
-            bf16x8 k8[KP], s8[WP];
-            kr[kb].planes(k8);
-#pragma unroll
-            for (int j = 0; j < WP; ++j)
-                s8[j] = *reinterpret_cast<const bf16x8*>(sS + (j * C + cg * 16 + l) * LK + 32 * kb + 8 * g);
-            mma_planes<KP, WP, WP>(k8, s8, aP);
-            if (!TRAIN) {
-                bf16x8 q8[KP];
-                qr[kb].planes(q8);
-                mma_planes<KP, WP, OP>(q8, s8, aQ);
-            }
-            if (cg == 0) {
-#pragma unroll
-                for (int j = 0; j < KP; ++j)
-                    *reinterpret_cast<bf16x8*>(sK + (j * 64 + irow) * LK + 32 * kb + 8 * g) = k8[j];
-            }
-        }
-        {
-            f32x4 R;
-#pragma unroll
-            for (int r = 0; r < 4; ++r) R[r] = fb[r] * v[r] - fp[r] * aP[r];
-            bf16x4 o[WP];
-            to_planes4<WP>(R, o);
-#pragma unroll
-            for (int j = 0; j < WP; ++j)
-                *reinterpret_cast<bf16x4*>(sR + (j * C + cg * 16 + l) * LT + drow) = o[j];
-        }
-        const f32x4 cu_ = fu, co_ = fo;
-        const float ceL = eL;
-        if (c + 1 < nch) {
-            load_k(c + 1);
-            if (!TRAIN) load_q(c + 1);
-            load_v(c + 1);
-            load_f(c + 1);
-        }
-        __syncthreads();
-        // stage 2
-        f32x4 aU = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-        for (int kb = 0; kb < 2; ++kb)
-            if (kb < nb) {
-                bf16x8 r8[WP];
-#pragma unroll
-                for (int j = 0; j < WP; ++j)
-                    r8[j] = *reinterpret_cast<const bf16x8*>(sR + (j * C + cg * 16 + l) * LT + 32 * kb + 8 * g);
-                mma_planes<WP, WP, WP>(tf[kb], r8, aU);
-            }
-        {
-            f32x4 u2;
-#pragma unroll
-            for (int r = 0; r < 4; ++r) u2[r] = cu_[r] * aU[r];
-            bf16x4 o[WP];
-            to_planes4<WP>(u2, o);
-#pragma unroll
-            for (int j = 0; j < WP; ++j)
-                *reinterpret_cast<bf16x4*>(sU2 + (j * C + cg * 16 + l) * LT + drow) = o[j];
-            if (!TRAIN) {
-                bf16x4 q[OP];
-                to_planes4<OP>(aU, q);
-#pragma unroll
-                for (int j = 0; j < OP; ++j)
-                    *reinterpret_cast<bf16x4*>(sU + (j * C + cg * 16 + l) * LT + drow) = q[j];
-            } else {
-#pragma unroll
-                for (int r = 0; r < 4; ++r) Ubuf[(ci * 64 + drow + r) * p.P + p0 + l] = aU[r];
-            }
-        }
-        if (c + 1 < nch) load_t(c + 1);
-        __syncthreads();
-        // stage 3
-#pragma unroll
-        for (int i = 0; i < TI; ++i) {
-            if (w + 4 * i >= NT) continue;
-            f32x4 acc = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-            for (int kb = 0; kb < 2; ++kb) {
-                bf16x8 u8[WP], kt[KP];
-#pragma unroll
-                for (int j = 0; j < WP; ++j)
-                    u8[j] = *reinterpret_cast<const bf16x8*>(sU2 + (j * C + cg * 16 + l) * LT + 32 * kb + 8 * g);
-#pragma unroll
-                for (int j = 0; j < KP; ++j) {
-                    const bf16* src = sK + (j * 64 + 32 * kb + 8 * g + (l >> 2)) * LK + 16 * (w + 4 * i) + 4 * (l & 3);
-                    const bf16x4 lo = lds_read_tr4(src), hi = lds_read_tr4(src + 4 * LK);
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) { kt[j][e] = lo[e]; kt[j][4 + e] = hi[e]; }
-                }
-                mma_planes<KP, WP, WP>(kt, u8, acc);
-            }
-#pragma unroll
-            for (int r = 0; r < 4; ++r) S[i][r] = ceL * S[i][r] + acc[r];
-        }
-        put_state();
-        if (!TRAIN) {
-            f32x4 aO;
-#pragma unroll
-            for (int r = 0; r < 4; ++r) aO[r] = co_[r] * aQ[r];
-#pragma unroll
-            for (int kb = 0; kb < 2; ++kb)
-                if (kb < nb) {
-                    bf16x8 u8[OP];
-#pragma unroll
-                    for (int j = 0; j < OP; ++j)
-                        u8[j] = *reinterpret_cast<const bf16x8*>(sU + (j * C + cg * 16 + l) * LT + 32 * kb + 8 * g);
-                    mma_planes<OP, OP, OP>(af[kb], u8, aO);
-                }
-#pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                const int64_t t = (int64_t)c * kDC + drow + r;
-                if (t < row.len) op[t * vs] = from_f32<IO>(aO[r]);
-            }
-            if (c + 1 < nch) load_a(c + 1);
-        }
-        __syncthreads();
-    }
-
-    if (!TRAIN && p.h_out != nullptr && rec >= 0) {
-#pragma unroll
-        for (int i = 0; i < TI; ++i)
-            if (w + 4 * i < NT)
-#pragma unroll
-                for (int r = 0; r < 4; ++r)
-                    p.h_out[((rec * p.H + h) * N + 16 * (w + 4 * i) + 4 * g + r) * p.P + p0 + l] = S[i][r];
-    }
-}
-
-template <typename F> hipError_t delta_allow_lds(F* kern, size_t bytes)
-{
-    const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(kern), hipFuncAttributeMaxDynamicSharedMemorySize,
-                                             (int)bytes);
-    (void)hipGetLastError();
-    return e;
+    wave_order();
+    put_lower<WP, LD>(p.tf + ci * (kTriBlocks * WP * 512), sM, l, g, lane);
+    if (BWD) put_upper<WP, LD>(ttf + ci * (kTriBlocks * WP * 512), sM, l, g, lane);
 }
 
 template <typename IO, int N, bool BWD>
@@ -585,20 +352,7 @@ hipError_t launch_delta_chunks(const DeltaParams& p, bf16* ttf, bf16* atf, hipSt
 {
     const int64_t blocks = (int64_t)p.rows * p.nc * p.H;
     if (blocks == 0) return hipSuccess;
-    hipLaunchKernelGGL((delta_chunk_kernel<IO, N, BWD>), dim3((unsigned)blocks), dim3(256), 0, stream, p, ttf, atf);
-    return hipGetLastError();
-}
-
-template <typename IO, int N, int NCG, bool TRAIN>
-hipError_t launch_delta_walk(const DeltaParams& p, float* Sbuf, float* Ubuf, hipStream_t stream)
-{
-    auto* const kern = &delta_walk_kernel<IO, N, NCG, TRAIN>;
-    constexpr size_t lds = WalkLds<IO, N, NCG>::bytes;
-    static const hipError_t attr = delta_allow_lds(kern, lds);
-    if (attr != hipSuccess) return attr;
-    const int64_t units = ((int64_t)p.rows * p.H + 7) / 8 * 8;
-    const int64_t blocks = units * (p.P / (16 * NCG));
-    hipLaunchKernelGGL(kern, dim3((unsigned)blocks), dim3(256 * NCG), lds, stream, p, Sbuf, Ubuf);
+    hipLaunchKernelGGL((delta_chunk_kernel<IO, N, BWD>), dim3((unsigned)blocks), dim3(64), 0, stream, p, ttf, atf);
     return hipGetLastError();
 }
 

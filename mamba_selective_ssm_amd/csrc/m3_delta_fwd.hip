@@ -1,5 +1,6 @@
 // Gated delta rule, prefill: chunk matrices, then the walk over the chunks.
 #include "m3_delta_chunk.hpp"
+#include "m3_delta_walk.hpp"
 
 namespace m3 {
 

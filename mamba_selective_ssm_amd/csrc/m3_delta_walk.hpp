@@ -1,0 +1,465 @@
+// Gated delta rule: the walk over a row's chunks.
+#pragma once
+
+#include "m3_delta.hpp"
+
+namespace m3 {
+
+// The walk over one row's chunks for one head and 16 NS columns of V.
+//
+// Per chunk:  R = beta V - sp (K S) | U = T R | S <- e^G_last S + K^T (d U),
+// and O = so (Q S) + A U with the chunk's first S.  Each product needs the one
+// before it, so the walk's time is this chain's, chunk after chunk, and all
+// that is not on it is kept out of it:
+//   - four state wavefronts per 16 columns run the chain, wave w on row tile w
+//     of each product; a result leaves as planes in operand order (tile_row),
+//     so that all four read it back with plain 16-byte reads after a barrier;
+//   - a loader wavefront moves K, T, V and the factors from memory straight to
+//     LDS, NBUF - 1 chunks ahead; they are first operands, the same for all
+//     columns;
+//   - two output wavefronts per 16 columns make O from the S and U planes, Q S
+//     while the state goes through T, A U during the next chunk's first stage.
+//
+// K rows lie in LDS in blocks of 8 values whose place is permuted by the row
+// (k_block), which keeps both the row-wise and the transposed reads free of
+// bank conflicts without padding, as the direct loads need it.
+template <typename IO, int N, int NS> struct WalkCfg {
+    static constexpr int KP = DeltaPlanes<IO>::io, WP = DeltaPlanes<IO>::wide, OP = DeltaPlanes<IO>::out;
+    static constexpr bool DIRECT = KP == 1;           // io values are operands as they are: loads go straight to LDS
+    static constexpr int NBUF = DIRECT ? 3 : 2;
+    static constexpr int KB = N / 32, NT = N / 16, TI = (NT + 3) / 4;
+    static constexpr int waves = 6 * NS + 1;
+    // bytes of one buffer (T apart: float32 calls have room for one T only)
+    static constexpr int k = 0, f = k + KP * 64 * N * 2, v = f + 5 * 256, buf = v + (DIRECT ? 64 * NS * 32 : 0);
+    static constexpr int tsize = kTriBlocks * WP * 1024, TB = DIRECT ? NBUF : 1;
+    static constexpr int t = NBUF * buf;
+    // then per column group the planes of S, R, d U, U
+    static constexpr int ex = t + TB * tsize, s = 0, r = s + WP * KB * 1024, u2 = r + WP * 2048, u = u2 + WP * 2048,
+                         ex1 = u + OP * 2048, total = ex + NS * ex1;
+    // loads of one chunk by the loader (DIRECT): T, factors, K, V
+    static constexpr int loads = kTriBlocks * WP + 2 + 64 * N * 2 / 1024 + 2 * NS;
+};
+
+// Where block j (8 values) of row t lies in its row.
+template <int N> __device__ __forceinline__ int k_block(int t, int j)
+{
+    if constexpr (N == 32) return j ^ ((t >> 3) & 3);
+    else if constexpr (N == 64) return j ^ (((t >> 1) & 1) | (((t >> 3) & 3) << 1));
+    else return j ^ ((t & 3) | (((t >> 3) & 3) << 2));
+}
+
+typedef __attribute__((address_space(3))) void lds_void;
+typedef __attribute__((address_space(1))) const void glb_void;
+
+// 16 (4) bytes a lane from memory to LDS at base + 16 (4) lane.
+__device__ __forceinline__ void to_lds16(char* base, const void* src)
+{
+    __builtin_amdgcn_global_load_lds((glb_void*)src, (lds_void*)base, 16, 0, 0);
+}
+__device__ __forceinline__ void to_lds4(char* base, const void* src)
+{
+    __builtin_amdgcn_global_load_lds((glb_void*)src, (lds_void*)base, 4, 0, 0);
+}
+// Waits until at most n of this wavefront's memory loads are in flight.
+template <int n> __device__ __forceinline__ void wait_loads()
+{
+    __builtin_amdgcn_s_waitcnt((n & 15) | ((n >> 4) << 14) | (7 << 4) | (15 << 8));
+}
+
+template <typename IO, int N, int NS, bool TRAIN>
+__global__ __launch_bounds__(64 * (6 * NS + 1)) void delta_walk_kernel(const DeltaParams p, float* Sbuf, float* Ubuf)
+{
+    using Cf = WalkCfg<IO, N, NS>;
+    constexpr int KP = Cf::KP, WP = Cf::WP, OP = Cf::OP, KB = Cf::KB, NT = Cf::NT, TI = Cf::TI, NBUF = Cf::NBUF;
+    extern __shared__ __attribute__((aligned(16))) char wlds[];
+
+    const int tid = threadIdx.x, lane = tid & 63, l = lane & 15, g = lane >> 4;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    // the slices of one (row, head) run on one XCD and share its L2
+    const int nsl = p.P / (16 * NS);
+    const int64_t idx = blockIdx.x >> 3;
+    const int64_t unit = (idx / nsl) * 8 + (blockIdx.x & 7);
+    if (unit >= (int64_t)p.rows * p.H) return;
+    int64_t b64, h64;
+    split_bh(unit, p.H, b64, h64);
+    const int b = (int)b64, h = (int)h64;
+    const int p0 = (int)(idx % nsl) * (16 * NS);   // first column of the workgroup
+    const DeltaRow row = delta_row(p, b);
+    const int64_t rec = TRAIN ? b : delta_record(p, b, tid, 64 * Cf::waves, reinterpret_cast<int*>(wlds));
+    const int nch = (int)((row.len + kDC - 1) / kDC);
+    const int rs = p.G * N, vs = p.H * p.P;
+    const int64_t ci0 = row.slot0 * p.H + h;
+    // Rows past the sequence's end read its last row instead: their beta is 0
+    // and T's rows there are the identity's, so they write and decay nothing.
+    const int nlast = (int)(row.len - (int64_t)(nch - 1) * kDC);   // tokens of the last chunk
+
+    if (wave == 6 * NS) {   // loader
+        const IO* kp = reinterpret_cast<const IO*>(p.k) + (row.start * p.G + h / (p.H / p.G)) * N;
+        const IO* vp = reinterpret_cast<const IO*>(p.v) + (row.start * p.H + h) * p.P + p0;
+        auto stage_t = [&](int c) {
+            char* dst = wlds + Cf::t + (c % Cf::TB) * Cf::tsize;
+            const char* src = reinterpret_cast<const char*>(p.tf + (ci0 + (int64_t)c * p.H) * (kTriBlocks * WP * 512));
+#pragma unroll
+            for (int i = 0; i < kTriBlocks * WP; ++i) to_lds16(dst + 1024 * i, src + 1024 * i + 16 * lane);
+        };
+        auto stage = [&](int c) {
+            char* buf = wlds + (c % NBUF) * Cf::buf;
+            const int end = c == nch - 1 ? nlast - 1 : kDC - 1;   // last row to read
+            const IO* kc = kp + (int64_t)c * kDC * rs;
+            constexpr int RPL = 512 / N;   // K rows of one load
+            const float* fsrc = p.sc + (ci0 + (int64_t)c * p.H) * (kDScal * 64);
+            to_lds16(buf + Cf::f, fsrc + 4 * lane);
+            to_lds4(buf + Cf::f + 1024, fsrc + 256 + lane);
+            if constexpr (Cf::DIRECT) {
+#pragma unroll
+                for (int i = 0; i < 64 / RPL; ++i) {
+                    const int t = RPL * i + lane / (N / 8), j = k_block<N>(t, lane % (N / 8));
+                    to_lds16(buf + Cf::k + 1024 * i, kc + (t < end ? t : end) * rs + 8 * j);
+                }
+                const IO* vc = vp + (int64_t)c * kDC * vs;
+                constexpr int VPL = 32 / NS;   // V rows of one load
+#pragma unroll
+                for (int i = 0; i < 2 * NS; ++i) {
+                    const int t = VPL * i + lane / (2 * NS);
+                    to_lds16(buf + Cf::v + 1024 * i, vc + (t < end ? t : end) * vs + 8 * (lane % (2 * NS)));
+                }
+                stage_t(c);
+            } else {
+#pragma unroll 4
+                for (int i = 0; i < 64 / RPL; ++i) {
+                    const int t = RPL * i + lane / (N / 8), j = k_block<N>(t, lane % (N / 8));
+                    RawRow8<IO> x;
+                    x.load(kc + (t < end ? t : end) * rs + 8 * j, true);
+                    bf16x8 o[KP];
+                    x.planes(o);
+#pragma unroll
+                    for (int q = 0; q < KP; ++q)
+                        *reinterpret_cast<bf16x8*>(buf + Cf::k + q * (64 * N * 2) + 1024 * i + 16 * lane) = o[q];
+                }
+            }
+        };
+        // s_barrier alone: the release of __syncthreads would wait for every load
+        auto barrier = [&]() {
+            asm volatile("" ::: "memory");
+            __builtin_amdgcn_s_barrier();
+            asm volatile("" ::: "memory");
+        };
+#pragma unroll
+        for (int c = 0; c < NBUF - 1; ++c)
+            if (c < nch) stage(c);
+        if (!Cf::DIRECT && nch > 0) stage_t(0);
+        asm volatile("" ::: "memory");
+        __builtin_amdgcn_s_waitcnt(0);
+        barrier();
+        for (int c = 0; c < nch; ++c) {
+            const bool more = c + NBUF - 1 < nch;
+            if (more) stage(c + NBUF - 1);
+            barrier();   // R
+            barrier();   // U: T is free
+            if (!Cf::DIRECT && c + 1 < nch) stage_t(c + 1);
+            asm volatile("" ::: "memory");
+            // the next chunk has landed
+            if (Cf::DIRECT && NBUF == 3 && more) wait_loads<Cf::loads>();
+            else __builtin_amdgcn_s_waitcnt(0);
+            barrier();   // S
+        }
+        return;
+    }
+
+    const f32x4 fz = {0.f, 0.f, 0.f, 0.f};
+    const int cg = wave < 4 * NS ? wave >> 2 : (wave - 4 * NS) >> 1;   // column group
+    char* ex = wlds + Cf::ex + cg * Cf::ex1 + 16 * lane;
+
+    if (wave >= 4 * NS) {   // output: row tiles 2 o, 2 o + 1
+        if (TRAIN) {
+            __syncthreads();
+            for (int c = 0; c < nch; ++c) {
+                __syncthreads();
+                __syncthreads();
+                __syncthreads();
+            }
+            return;
+        }
+        const int o = wave & 1;
+        const IO* qp = reinterpret_cast<const IO*>(p.q) + (row.start * p.G + h / (p.H / p.G)) * N + 8 * g;
+        IO* op = reinterpret_cast<IO*>(p.o) + (row.start * p.H + h) * p.P + p0 + 16 * cg + l;
+        RawRow8<IO> q[2][KB];
+        bf16x8 a0[2][OP], a1[2][OP];
+        f32x4 fo[2], acc[2] = {fz, fz};
+        auto load = [&](int c) {
+            const int end = c == nch - 1 ? nlast - 1 : kDC - 1;
+            const IO* qc = qp + (int64_t)c * kDC * rs;
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const int t = tile_row(2 * o + i, l) < end ? tile_row(2 * o + i, l) : end;
+#pragma unroll
+                for (int kb = 0; kb < KB; ++kb) q[i][kb].load(qc + t * rs + 32 * kb, true);
+            }
+            const float* f = p.sc + (ci0 + (int64_t)c * p.H) * (kDScal * 64) + 192 + 8 * g;
+#pragma unroll
+            for (int i = 0; i < 2; ++i) fo[i] = *reinterpret_cast<const f32x4*>(f + 32 * o + 4 * i);
+        };
+        auto load_a = [&](int c) {   // blocks (2 o + i, 0), and (2 + i, 1) of the lower tiles
+            const bf16* src = p.af + (ci0 + (int64_t)c * p.H) * (kTriBlocks * OP * 512) + lane * 8;
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+#pragma unroll
+                for (int j = 0; j < OP; ++j) {
+                    a0[i][j] = *reinterpret_cast<const bf16x8*>(src + ((2 * o + i) * OP + j) * 512);
+                    a1[i][j] = *reinterpret_cast<const bf16x8*>(src + ((4 + i) * OP + j) * 512);
+                }
+        };
+        auto finish = [&](int c) {   // A U of chunk c, and its rows of O
+            bf16x8 u8[OP];
+#pragma unroll
+            for (int j = 0; j < OP; ++j) u8[j] = *reinterpret_cast<const bf16x8*>(ex + Cf::u + 2 * j * 1024);
+            mma_tiles<2, OP, OP, OP>(a0, u8, acc);
+            if (o) {
+#pragma unroll
+                for (int j = 0; j < OP; ++j) u8[j] = *reinterpret_cast<const bf16x8*>(ex + Cf::u + (2 * j + 1) * 1024);
+                mma_tiles<2, OP, OP, OP>(a1, u8, acc);
+            }
+            const int nv = c == nch - 1 ? nlast : kDC;
+            IO* oc = op + (int64_t)c * kDC * vs;
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    const int t = 32 * o + 8 * g + 4 * i + r;
+                    if (t < nv) oc[t * vs] = from_f32<IO>(acc[i][r]);
+                }
+        };
+        if (nch > 0) {
+            load(0);
+            load_a(0);
+        }
+        __syncthreads();
+        for (int c = 0; c < nch; ++c) {
+            if (c > 0) {
+                finish(c - 1);
+                load_a(c);
+            }
+            __syncthreads();   // R
+            acc[0] = fz;
+            acc[1] = fz;
+#pragma unroll
+            for (int kb = 0; kb < KB; ++kb) {
+                bf16x8 s8[OP], q8[2][KP];
+#pragma unroll
+                for (int j = 0; j < OP; ++j) s8[j] = *reinterpret_cast<const bf16x8*>(ex + Cf::s + (j * KB + kb) * 1024);
+#pragma unroll
+                for (int i = 0; i < 2; ++i) q[i][kb].planes(q8[i]);
+                mma_tiles<2, KP, OP, OP>(q8, s8, acc);
+            }
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+#pragma unroll
+                for (int r = 0; r < 4; ++r) acc[i][r] *= fo[i][r];
+            if (c + 1 < nch) load(c + 1);
+            __syncthreads();   // U
+            __syncthreads();   // S
+        }
+        if (nch > 0) finish(nch - 1);
+        return;
+    }
+
+    // state: wave w has tile w of R and U and tiles w, w + 4 of the state, rows
+    // tile_row(tile, 4 g + r), column l
+    const int w = wave & 3;
+    const int tr0 = 32 * (w >> 1) + 4 * (w & 1) + 8 * g;   // first row of tile w in this lane
+    const int nb = (w >> 1) + 1;                           // 32-token blocks that tile w of T spans
+    const int half = 8 * (w & 1);                          // its place in an operand's 16 bytes
+    const int col = p0 + 16 * cg + l;
+    f32x4 S[TI];
+    const float* hin = p.h_in != nullptr && rec >= 0 ? p.h_in + (rec * p.H + h) * (int64_t)(N * p.P) + col : nullptr;
+#pragma unroll
+    for (int i = 0; i < TI; ++i)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+            S[i][r] = hin != nullptr && w + 4 * i < NT ? hin[(tr0 + 64 * i + r) * p.P] : 0.f;
+            if (rec == -2) S[i][r] = __builtin_nanf("");   // the record belongs to an earlier row
+        }
+    auto put_state = [&]() {
+#pragma unroll
+        for (int i = 0; i < TI; ++i) {
+            if (w + 4 * i >= NT) continue;
+            bf16x4 o[WP];
+            to_planes4<WP>(S[i], o);
+#pragma unroll
+            for (int j = 0; j < WP; ++j)
+                *reinterpret_cast<bf16x4*>(ex + Cf::s + (j * KB + 2 * i + (w >> 1)) * 1024 + half) = o[j];
+        }
+    };
+    put_state();
+
+    // V of float32 calls comes from memory one chunk ahead, of bf16 calls from LDS
+    const IO* vp = reinterpret_cast<const IO*>(p.v) + (row.start * p.H + h) * p.P + col;
+    float vnext[4];
+    auto load_v = [&](int c) {
+        if constexpr (!Cf::DIRECT) {
+            const int end = c == nch - 1 ? nlast - 1 : kDC - 1;
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+                vnext[r] = to_f32(vp[(int64_t)c * kDC * vs + (tr0 + r < end ? tr0 + r : end) * vs]);
+        }
+    };
+    if (nch > 0) load_v(0);
+    __syncthreads();
+
+    for (int c = 0; c < nch; ++c) {
+        const char* buf = wlds + (c % NBUF) * Cf::buf;
+        const int64_t ci = ci0 + (int64_t)c * p.H;
+        if (TRAIN) {
+            float* sd = Sbuf + ci * N * p.P + col;
+#pragma unroll
+            for (int i = 0; i < TI; ++i)
+                if (w + 4 * i < NT)
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) sd[(tr0 + 64 * i + r) * p.P] = S[i][r];
+        }
+        // R = beta V - sp (K S)
+        const float* f = reinterpret_cast<const float*>(buf + Cf::f) + tr0;
+        f32x4 P = fz;
+        {
+            const int t = tile_row(w, l);
+            bf16x8 k8[KB][KP], s8[KB][WP];
+#pragma unroll
+            for (int kb = 0; kb < KB; ++kb) {
+#pragma unroll
+                for (int j = 0; j < WP; ++j) s8[kb][j] = *reinterpret_cast<const bf16x8*>(ex + Cf::s + (j * KB + kb) * 1024);
+#pragma unroll
+                for (int j = 0; j < KP; ++j)
+                    k8[kb][j] = *reinterpret_cast<const bf16x8*>(buf + Cf::k + j * (64 * N * 2) + t * (2 * N) +
+                                                                 16 * k_block<N>(t, 4 * kb + g));
+            }
+            const f32x4 fb = *reinterpret_cast<const f32x4*>(f), fp = *reinterpret_cast<const f32x4*>(f + 64);
+            float v[4];
+            if constexpr (Cf::DIRECT) {
+                const bf16x4 x = lds_read_tr4(reinterpret_cast<const bf16*>(buf + Cf::v) +
+                                              (tr0 + (l >> 2)) * (16 * NS) + 16 * cg + 4 * (l & 3));
+#pragma unroll
+                for (int r = 0; r < 4; ++r) v[r] = (float)x[r];
+            } else {
+#pragma unroll
+                for (int r = 0; r < 4; ++r) v[r] = vnext[r];
+            }
+#pragma unroll
+            for (int kb = 0; kb < KB; ++kb) mma_planes<KP, WP, WP>(k8[kb], s8[kb], P);
+            f32x4 R;
+#pragma unroll
+            for (int r = 0; r < 4; ++r) R[r] = fb[r] * v[r] - fp[r] * P[r];
+            bf16x4 o[WP];
+            to_planes4<WP>(R, o);
+#pragma unroll
+            for (int j = 0; j < WP; ++j) *reinterpret_cast<bf16x4*>(ex + Cf::r + (2 * j + (w >> 1)) * 1024 + half) = o[j];
+        }
+        if (c + 1 < nch) load_v(c + 1);
+        // first operands of the next two products, on their way across the barriers
+        bf16x8 t8[2][WP];
+        const char* tb = wlds + Cf::t + (c % Cf::TB) * Cf::tsize + 16 * lane;
+#pragma unroll
+        for (int kb = 0; kb < 2; ++kb)
+#pragma unroll
+            for (int j = 0; j < WP; ++j)
+                t8[kb][j] = *reinterpret_cast<const bf16x8*>(tb + (low_block(w, kb < nb ? kb : 0) * WP + j) * 1024);
+        const f32x4 fu = *reinterpret_cast<const f32x4*>(f + 128);
+        const float eL = *reinterpret_cast<const float*>(buf + Cf::f + 1024 + 4 * lane);
+        __syncthreads();
+        // U = T R
+        f32x4 U = fz;
+#pragma unroll
+        for (int kb = 0; kb < 2; ++kb)
+            if (kb < nb) {
+                bf16x8 r8[WP];
+#pragma unroll
+                for (int j = 0; j < WP; ++j) r8[j] = *reinterpret_cast<const bf16x8*>(ex + Cf::r + (2 * j + kb) * 1024);
+                mma_planes<WP, WP, WP>(t8[kb], r8, U);
+            }
+        {
+            f32x4 u2;
+#pragma unroll
+            for (int r = 0; r < 4; ++r) u2[r] = fu[r] * U[r];
+            bf16x4 o[WP];
+            to_planes4<WP>(u2, o);
+#pragma unroll
+            for (int j = 0; j < WP; ++j) *reinterpret_cast<bf16x4*>(ex + Cf::u2 + (2 * j + (w >> 1)) * 1024 + half) = o[j];
+            if (!TRAIN) {
+                bf16x4 q[OP];
+                to_planes4<OP>(U, q);
+#pragma unroll
+                for (int j = 0; j < OP; ++j) *reinterpret_cast<bf16x4*>(ex + Cf::u + (2 * j + (w >> 1)) * 1024 + half) = q[j];
+            } else {
+#pragma unroll
+                for (int r = 0; r < 4; ++r) Ubuf[(ci * 64 + tr0 + r) * p.P + col] = U[r];
+            }
+        }
+        bf16x8 kt[TI][2][KP];
+#pragma unroll
+        for (int i = 0; i < TI; ++i)
+#pragma unroll
+            for (int kb = 0; kb < 2; ++kb) {
+                const int t = 32 * kb + 8 * g + (l >> 2), j4 = w + 4 * i < NT ? 4 * (2 * i + (w >> 1)) + (l & 3) : 0;
+#pragma unroll
+                for (int j = 0; j < KP; ++j) {
+                    const char* src = buf + Cf::k + j * (64 * N * 2) + half;
+                    kt[i][kb][j] = join8(lds_read_tr4(reinterpret_cast<const bf16*>(src + t * (2 * N) + 16 * k_block<N>(t, j4))),
+                                         lds_read_tr4(reinterpret_cast<const bf16*>(src + (t + 4) * (2 * N) + 16 * k_block<N>(t + 4, j4))));
+                }
+            }
+        __syncthreads();
+        // S <- e^G_last S + K^T (d U)
+        f32x4 acc[TI];
+#pragma unroll
+        for (int i = 0; i < TI; ++i) acc[i] = fz;
+#pragma unroll
+        for (int kb = 0; kb < 2; ++kb) {
+            bf16x8 u8[WP], k8[TI][KP];
+#pragma unroll
+            for (int j = 0; j < WP; ++j) u8[j] = *reinterpret_cast<const bf16x8*>(ex + Cf::u2 + (2 * j + kb) * 1024);
+#pragma unroll
+            for (int i = 0; i < TI; ++i)
+#pragma unroll
+                for (int j = 0; j < KP; ++j) k8[i][j] = kt[i][kb][j];
+            mma_tiles<TI, KP, WP, WP>(k8, u8, acc);
+        }
+#pragma unroll
+        for (int i = 0; i < TI; ++i)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) S[i][r] = eL * S[i][r] + acc[i][r];
+        put_state();
+        __syncthreads();
+    }
+    if (!TRAIN && p.h_out != nullptr && rec >= 0) {
+        float* ho = p.h_out + (rec * p.H + h) * (int64_t)(N * p.P) + col;
+#pragma unroll
+        for (int i = 0; i < TI; ++i)
+            if (w + 4 * i < NT)
+#pragma unroll
+                for (int r = 0; r < 4; ++r) ho[(tr0 + 64 * i + r) * p.P] = S[i][r];
+    }
+}
+
+template <typename F> hipError_t delta_allow_lds(F* kern, size_t bytes)
+{
+    const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(kern), hipFuncAttributeMaxDynamicSharedMemorySize,
+                                             (int)bytes);
+    (void)hipGetLastError();
+    return e;
+}
+
+template <typename IO, int N, int NS, bool TRAIN>
+hipError_t launch_delta_walk(const DeltaParams& p, float* Sbuf, float* Ubuf, hipStream_t stream)
+{
+    auto* const kern = &delta_walk_kernel<IO, N, NS, TRAIN>;
+    constexpr size_t lds = WalkCfg<IO, N, NS>::total;
+    static_assert(lds <= 160 * 1024, "a workgroup's LDS");
+    static const hipError_t attr = delta_allow_lds(kern, lds);
+    if (attr != hipSuccess) return attr;
+    const int64_t units = ((int64_t)p.rows * p.H + 7) / 8 * 8;
+    const int64_t blocks = units * (p.P / (16 * NS));
+    constexpr int threads = 64 * WalkCfg<IO, N, NS>::waves;
+    hipLaunchKernelGGL(kern, dim3((unsigned)blocks), dim3(threads), lds, stream, p, Sbuf, Ubuf);
+    return hipGetLastError();
+}
+
+}  // namespace m3
