@@ -98,6 +98,15 @@ __host__ __device__ constexpr int up_block(int w, int kb) { return w + 2 * kb; }
 
 inline size_t delta_tri_elems(int planes) { return (size_t)kTriBlocks * planes * 512; }
 
+// What a wavefront's lanes have written to LDS before is there for all its
+// lanes after: its LDS instructions run in order, so only the compiler's order
+// has to be held.
+__device__ __forceinline__ void wave_order()
+{
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+}
+
 // Where a row's tokens lie: its first token row, its length, its first chunk
 // slot.  Offsets are clamped into the arrays and lengths to max_len, so that
 // wrong ones give wrong results and no access outside.

@@ -22,15 +22,6 @@ __device__ __forceinline__ void tile_put(float* C, int l, int g, const f32x4& v)
     for (int r = 0; r < 4; ++r) C[(4 * g + r) * LD + l] = v[r];
 }
 
-// What a wavefront's lanes have written to LDS before is there for all its
-// lanes after: its LDS instructions run in order, so only the compiler's order
-// has to be held.
-__device__ __forceinline__ void wave_order()
-{
-    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-    __builtin_amdgcn_wave_barrier();
-}
-
 // Inclusive prefix sum across a wavefront in float64, by the lane moves of
 // wave_inclusive_sum on both halves.
 template <int CTRL, int ROW_MASK> __device__ __forceinline__ double dpp_moved_d(double x)

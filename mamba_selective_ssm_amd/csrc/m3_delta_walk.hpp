@@ -1,6 +1,8 @@
 // Gated delta rule: the walk over a row's chunks.
 #pragma once
 
+#include <type_traits>
+
 #include "m3_delta.hpp"
 
 namespace m3 {
@@ -33,9 +35,9 @@ template <typename IO, int N, int NS> struct WalkCfg {
     static constexpr int k = 0, f = k + KP * 64 * N * 2, v = f + 5 * 256, buf = v + (DIRECT ? 64 * NS * 32 : 0);
     static constexpr int tsize = kTriBlocks * WP * 1024, TB = DIRECT ? NBUF : 1;
     static constexpr int t = NBUF * buf;
-    // then per column group the planes of S, R, d U, U
+    // then per column group the planes of S, R, d U, U, and the rows of O
     static constexpr int ex = t + TB * tsize, s = 0, r = s + WP * KB * 1024, u2 = r + WP * 2048, u = u2 + WP * 2048,
-                         ex1 = u + OP * 2048, total = ex + NS * ex1;
+                         o = u + OP * 2048, ex1 = o + 64 * 16 * (int)sizeof(IO), total = ex + NS * ex1;
     // loads of one chunk by the loader (DIRECT): T, factors, K, V
     static constexpr int loads = kTriBlocks * WP + 2 + 64 * N * 2 / 1024 + 2 * NS;
 };
@@ -96,11 +98,12 @@ __global__ __launch_bounds__(64 * (6 * NS + 1)) void delta_walk_kernel(const Del
     if (wave == 6 * NS) {   // loader
         const IO* kp = reinterpret_cast<const IO*>(p.k) + (row.start * p.G + h / (p.H / p.G)) * N;
         const IO* vp = reinterpret_cast<const IO*>(p.v) + (row.start * p.H + h) * p.P + p0;
-        auto stage_t = [&](int c) {
+        auto stage_t = [&](int c, int i0, int i1) {   // blocks i0..i1-1 of T
             char* dst = wlds + Cf::t + (c % Cf::TB) * Cf::tsize;
             const char* src = reinterpret_cast<const char*>(p.tf + (ci0 + (int64_t)c * p.H) * (kTriBlocks * WP * 512));
 #pragma unroll
-            for (int i = 0; i < kTriBlocks * WP; ++i) to_lds16(dst + 1024 * i, src + 1024 * i + 16 * lane);
+            for (int i = 0; i < kTriBlocks * WP; ++i)
+                if (i >= i0 && i < i1) to_lds16(dst + 1024 * i, src + 1024 * i + 16 * lane);
         };
         auto stage = [&](int c) {
             char* buf = wlds + (c % NBUF) * Cf::buf;
@@ -123,7 +126,6 @@ __global__ __launch_bounds__(64 * (6 * NS + 1)) void delta_walk_kernel(const Del
                     const int t = VPL * i + lane / (2 * NS);
                     to_lds16(buf + Cf::v + 1024 * i, vc + (t < end ? t : end) * vs + 8 * (lane % (2 * NS)));
                 }
-                stage_t(c);
             } else {
 #pragma unroll 4
                 for (int i = 0; i < 64 / RPL; ++i) {
@@ -146,17 +148,26 @@ __global__ __launch_bounds__(64 * (6 * NS + 1)) void delta_walk_kernel(const Del
         };
 #pragma unroll
         for (int c = 0; c < NBUF - 1; ++c)
-            if (c < nch) stage(c);
-        if (!Cf::DIRECT && nch > 0) stage_t(0);
+            if (c < nch) {
+                stage(c);
+                if (c < Cf::TB) stage_t(c, 0, 3 * kTriBlocks);
+            }
         asm volatile("" ::: "memory");
         __builtin_amdgcn_s_waitcnt(0);
         barrier();
         for (int c = 0; c < nch; ++c) {
+            // a third of the loads beside each stage: a load takes some 30
+            // cycles to issue, all of one chunk longer than a stage
             const bool more = c + NBUF - 1 < nch;
             if (more) stage(c + NBUF - 1);
             barrier();   // R
-            barrier();   // U: T is free
-            if (!Cf::DIRECT && c + 1 < nch) stage_t(c + 1);
+            if (Cf::DIRECT && more) stage_t(c + NBUF - 1, 0, 9);
+            barrier();   // U: a single T is free
+            if (Cf::DIRECT) {
+                if (more) stage_t(c + NBUF - 1, 9, 18);
+            } else if (c + 1 < nch) {
+                stage_t(c + 1, 0, 18);
+            }
             asm volatile("" ::: "memory");
             // the next chunk has landed
             if (Cf::DIRECT && NBUF == 3 && more) wait_loads<Cf::loads>();
@@ -180,13 +191,20 @@ __global__ __launch_bounds__(64 * (6 * NS + 1)) void delta_walk_kernel(const Del
             }
             return;
         }
-        const int o = wave & 1;
+        // No load depends on a branch: where one might, a wait for the chunk's
+        // operands would also wait for those of the chunk after it.
+        auto output = [&](auto half_) {
+        constexpr int o = decltype(half_)::value;
         const IO* qp = reinterpret_cast<const IO*>(p.q) + (row.start * p.G + h / (p.H / p.G)) * N + 8 * g;
-        IO* op = reinterpret_cast<IO*>(p.o) + (row.start * p.H + h) * p.P + p0 + 16 * cg + l;
+        IO* op = reinterpret_cast<IO*>(p.o) + (row.start * p.H + h) * p.P + p0 + 16 * cg;
+        IO* so = reinterpret_cast<IO*>(wlds + Cf::ex + cg * Cf::ex1 + Cf::o) + 32 * o * 16;   // this wave's rows
         RawRow8<IO> q[2][KB];
-        bf16x8 a0[2][OP], a1[2][OP];
-        f32x4 fo[2], acc[2] = {fz, fz};
+        struct Tri {
+            bf16x8 a0[2][OP], a1[2][OP];
+        } ta, tb;
+        f32x4 acc[2] = {fz, fz}, out[2];
         auto load = [&](int c) {
+            c = c < nch ? c : nch - 1;
             const int end = c == nch - 1 ? nlast - 1 : kDC - 1;
             const IO* qc = qp + (int64_t)c * kDC * rs;
 #pragma unroll
@@ -195,53 +213,63 @@ __global__ __launch_bounds__(64 * (6 * NS + 1)) void delta_walk_kernel(const Del
 #pragma unroll
                 for (int kb = 0; kb < KB; ++kb) q[i][kb].load(qc + t * rs + 32 * kb, true);
             }
-            const float* f = p.sc + (ci0 + (int64_t)c * p.H) * (kDScal * 64) + 192 + 8 * g;
-#pragma unroll
-            for (int i = 0; i < 2; ++i) fo[i] = *reinterpret_cast<const f32x4*>(f + 32 * o + 4 * i);
         };
-        auto load_a = [&](int c) {   // blocks (2 o + i, 0), and (2 + i, 1) of the lower tiles
+        auto load_a = [&](Tri& x, int c) {   // blocks (2 o + i, 0), and (2 + i, 1) of the lower tiles
+            c = c < nch ? c : nch - 1;
             const bf16* src = p.af + (ci0 + (int64_t)c * p.H) * (kTriBlocks * OP * 512) + lane * 8;
 #pragma unroll
             for (int i = 0; i < 2; ++i)
 #pragma unroll
-                for (int j = 0; j < OP; ++j) {
-                    a0[i][j] = *reinterpret_cast<const bf16x8*>(src + ((2 * o + i) * OP + j) * 512);
-                    a1[i][j] = *reinterpret_cast<const bf16x8*>(src + ((4 + i) * OP + j) * 512);
-                }
+                for (int j = 0; j < OP; ++j) x.a0[i][j] = *reinterpret_cast<const bf16x8*>(src + ((2 * o + i) * OP + j) * 512);
+            if (o)
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+#pragma unroll
+                    for (int j = 0; j < OP; ++j) x.a1[i][j] = *reinterpret_cast<const bf16x8*>(src + ((4 + i) * OP + j) * 512);
         };
-        auto finish = [&](int c) {   // A U of chunk c, and its rows of O
-            bf16x8 u8[OP];
+        auto add_u = [&](const Tri& x) {   // + A U
 #pragma unroll
-            for (int j = 0; j < OP; ++j) u8[j] = *reinterpret_cast<const bf16x8*>(ex + Cf::u + 2 * j * 1024);
-            mma_tiles<2, OP, OP, OP>(a0, u8, acc);
-            if (o) {
+            for (int i = 0; i < 2; ++i) out[i] = acc[i];
+            bf16x8 u8[2][OP];
 #pragma unroll
-                for (int j = 0; j < OP; ++j) u8[j] = *reinterpret_cast<const bf16x8*>(ex + Cf::u + (2 * j + 1) * 1024);
-                mma_tiles<2, OP, OP, OP>(a1, u8, acc);
-            }
-            const int nv = c == nch - 1 ? nlast : kDC;
-            IO* oc = op + (int64_t)c * kDC * vs;
+            for (int kb = 0; kb < 2; ++kb)
+#pragma unroll
+                for (int j = 0; j < OP; ++j) u8[kb][j] = *reinterpret_cast<const bf16x8*>(ex + Cf::u + (2 * j + kb) * 1024);
+            mma_tiles<2, OP, OP, OP>(x.a0, u8[0], out);
+            if (o) mma_tiles<2, OP, OP, OP>(x.a1, u8[1], out);
+        };
+        auto store = [&](int c) {   // through LDS: 16 bytes of a row to a lane, not 2
 #pragma unroll
             for (int i = 0; i < 2; ++i)
 #pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    const int t = 32 * o + 8 * g + 4 * i + r;
-                    if (t < nv) oc[t * vs] = from_f32<IO>(acc[i][r]);
-                }
+                for (int r = 0; r < 4; ++r) so[(8 * g + 4 * i + r) * 16 + l] = from_f32<IO>(out[i][r]);
+            wave_order();
+            const int nv = c == nch - 1 ? nlast : kDC;
+            IO* oc = op + (int64_t)c * kDC * vs;
+            constexpr int per = 16 / sizeof(IO), lpr = 16 / per;   // values to a lane, lanes to a row
+#pragma unroll
+            for (int i = 0; i < lpr / 2; ++i) {
+                const int t = (64 / lpr) * i + lane / lpr, j = lane % lpr;
+                const uint4 x = *reinterpret_cast<const uint4*>(so + t * 16 + per * j);
+                if (32 * o + t < nv) *reinterpret_cast<uint4*>(oc + (32 * o + t) * vs + per * j) = x;
+            }
+            wave_order();
         };
         if (nch > 0) {
             load(0);
-            load_a(0);
+            load_a(ta, 0);
+            load_a(tb, 0);
         }
         __syncthreads();
-        for (int c = 0; c < nch; ++c) {
-            if (c > 0) {
-                finish(c - 1);
-                load_a(c);
-            }
+        auto step = [&](Tri& cur, Tri& prev, int c) {
+            add_u(prev);   // (the first chunk's goes nowhere)
             __syncthreads();   // R
             acc[0] = fz;
             acc[1] = fz;
+            f32x4 fo[2];
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+                fo[i] = *reinterpret_cast<const f32x4*>(wlds + (c % NBUF) * Cf::buf + Cf::f + 4 * (192 + 32 * o + 8 * g + 4 * i));
 #pragma unroll
             for (int kb = 0; kb < KB; ++kb) {
                 bf16x8 s8[OP], q8[2][KP];
@@ -255,11 +283,24 @@ __global__ __launch_bounds__(64 * (6 * NS + 1)) void delta_walk_kernel(const Del
             for (int i = 0; i < 2; ++i)
 #pragma unroll
                 for (int r = 0; r < 4; ++r) acc[i][r] *= fo[i][r];
-            if (c + 1 < nch) load(c + 1);
+            load(c + 1);
             __syncthreads();   // U
+            load_a(prev, c + 1);
+            if (c > 0) store(c - 1);
             __syncthreads();   // S
+        };
+        for (int c = 0; c < nch; c += 2) {
+            step(ta, tb, c);
+            if (c + 1 < nch) step(tb, ta, c + 1);
         }
-        if (nch > 0) finish(nch - 1);
+        if (nch > 0) {
+            if (nch & 1) add_u(ta);
+            else add_u(tb);
+            store(nch - 1);
+        }
+        };
+        if (wave & 1) output(std::integral_constant<int, 1>());
+        else output(std::integral_constant<int, 0>());
         return;
     }
 
@@ -319,6 +360,10 @@ __global__ __launch_bounds__(64 * (6 * NS + 1)) void delta_walk_kernel(const Del
         }
         // R = beta V - sp (K S)
         const float* f = reinterpret_cast<const float*>(buf + Cf::f) + tr0;
+        const char* tb = wlds + Cf::t + (c % Cf::TB) * Cf::tsize + 16 * lane;
+        bf16x8 t8[2][WP];   // T's rows, read beside the other operands
+        const f32x4 fu = *reinterpret_cast<const f32x4*>(f + 128);
+        const float eL = *reinterpret_cast<const float*>(buf + Cf::f + 1024 + 4 * lane);
         f32x4 P = fz;
         {
             const int t = tile_row(w, l);
@@ -332,6 +377,11 @@ __global__ __launch_bounds__(64 * (6 * NS + 1)) void delta_walk_kernel(const Del
                     k8[kb][j] = *reinterpret_cast<const bf16x8*>(buf + Cf::k + j * (64 * N * 2) + t * (2 * N) +
                                                                  16 * k_block<N>(t, 4 * kb + g));
             }
+#pragma unroll
+            for (int kb = 0; kb < 2; ++kb)
+#pragma unroll
+                for (int j = 0; j < WP; ++j)
+                    t8[kb][j] = *reinterpret_cast<const bf16x8*>(tb + (low_block(w, kb < nb ? kb : 0) * WP + j) * 1024);
             const f32x4 fb = *reinterpret_cast<const f32x4*>(f), fp = *reinterpret_cast<const f32x4*>(f + 64);
             float v[4];
             if constexpr (Cf::DIRECT) {
@@ -354,19 +404,22 @@ __global__ __launch_bounds__(64 * (6 * NS + 1)) void delta_walk_kernel(const Del
             for (int j = 0; j < WP; ++j) *reinterpret_cast<bf16x4*>(ex + Cf::r + (2 * j + (w >> 1)) * 1024 + half) = o[j];
         }
         if (c + 1 < nch) load_v(c + 1);
-        // first operands of the next two products, on their way across the barriers
-        bf16x8 t8[2][WP];
-        const char* tb = wlds + Cf::t + (c % Cf::TB) * Cf::tsize + 16 * lane;
-#pragma unroll
-        for (int kb = 0; kb < 2; ++kb)
-#pragma unroll
-            for (int j = 0; j < WP; ++j)
-                t8[kb][j] = *reinterpret_cast<const bf16x8*>(tb + (low_block(w, kb < nb ? kb : 0) * WP + j) * 1024);
-        const f32x4 fu = *reinterpret_cast<const f32x4*>(f + 128);
-        const float eL = *reinterpret_cast<const float*>(buf + Cf::f + 1024 + 4 * lane);
         __syncthreads();
         // U = T R
         f32x4 U = fz;
+        bf16x8 kt[TI][2][KP];
+#pragma unroll
+        for (int i = 0; i < TI; ++i)
+#pragma unroll
+            for (int kb = 0; kb < 2; ++kb) {
+                const int t = 32 * kb + 8 * g + (l >> 2), j4 = w + 4 * i < NT ? 4 * (2 * i + (w >> 1)) + (l & 3) : 0;
+#pragma unroll
+                for (int j = 0; j < KP; ++j) {
+                    const char* src = buf + Cf::k + j * (64 * N * 2) + half;
+                    kt[i][kb][j] = join8(lds_read_tr4(reinterpret_cast<const bf16*>(src + t * (2 * N) + 16 * k_block<N>(t, j4))),
+                                         lds_read_tr4(reinterpret_cast<const bf16*>(src + (t + 4) * (2 * N) + 16 * k_block<N>(t + 4, j4))));
+                }
+            }
 #pragma unroll
         for (int kb = 0; kb < 2; ++kb)
             if (kb < nb) {
@@ -393,19 +446,6 @@ __global__ __launch_bounds__(64 * (6 * NS + 1)) void delta_walk_kernel(const Del
                 for (int r = 0; r < 4; ++r) Ubuf[(ci * 64 + tr0 + r) * p.P + col] = U[r];
             }
         }
-        bf16x8 kt[TI][2][KP];
-#pragma unroll
-        for (int i = 0; i < TI; ++i)
-#pragma unroll
-            for (int kb = 0; kb < 2; ++kb) {
-                const int t = 32 * kb + 8 * g + (l >> 2), j4 = w + 4 * i < NT ? 4 * (2 * i + (w >> 1)) + (l & 3) : 0;
-#pragma unroll
-                for (int j = 0; j < KP; ++j) {
-                    const char* src = buf + Cf::k + j * (64 * N * 2) + half;
-                    kt[i][kb][j] = join8(lds_read_tr4(reinterpret_cast<const bf16*>(src + t * (2 * N) + 16 * k_block<N>(t, j4))),
-                                         lds_read_tr4(reinterpret_cast<const bf16*>(src + (t + 4) * (2 * N) + 16 * k_block<N>(t + 4, j4))));
-                }
-            }
         __syncthreads();
         // S <- e^G_last S + K^T (d U)
         f32x4 acc[TI];
