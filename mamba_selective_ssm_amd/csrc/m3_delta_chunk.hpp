@@ -107,7 +107,7 @@ template <int PL, int LD> __device__ __forceinline__ void put_upper(bf16* dst, c
 // zero.  Rows past the end read the last row again; their beta is 0 and their
 // g is 0, which makes their rows of T the identity's.
 template <typename IO, int N, bool BWD>
-__global__ __launch_bounds__(64) void delta_chunk_kernel(const DeltaParams p, bf16* ttf, bf16* atf)
+__global__ __launch_bounds__(64, 2) void delta_chunk_kernel(const DeltaParams p, bf16* ttf, bf16* atf)
 {
     constexpr int KP = DeltaPlanes<IO>::io, WP = DeltaPlanes<IO>::wide, OP = DeltaPlanes<IO>::out;
     constexpr int AP = BWD ? WP : OP;     // the gradient's path is float32 throughout
@@ -133,7 +133,7 @@ __global__ __launch_bounds__(64) void delta_chunk_kernel(const DeltaParams p, bf
     const int tok = lane < nv ? lane : nv - 1;
     float gv = p.g[(t0 + tok) * p.H + h];
     float bv = p.beta[(t0 + tok) * p.H + h];
-    RawRow8<IO> kr[4][KB], qr[KB];
+    RawRow8<IO> kr[4][KB], qr[4][KB];
     int off[4];
 #pragma unroll
     for (int rt = 0; rt < 4; ++rt) {
@@ -142,8 +142,12 @@ __global__ __launch_bounds__(64) void delta_chunk_kernel(const DeltaParams p, bf
 #pragma unroll
         for (int kb = 0; kb < KB; ++kb) kr[rt][kb].load(kp + off[rt] + 32 * kb, true);
     }
+    // the larger rows would not fit beside K's: they are read tile by tile
+    constexpr bool ALLQ = KP == 1 && N < 128;
 #pragma unroll
-    for (int kb = 0; kb < KB; ++kb) qr[kb].load(qp + off[0] + 32 * kb, true);
+    for (int rt = 0; rt < (ALLQ ? 4 : 1); ++rt)
+#pragma unroll
+        for (int kb = 0; kb < KB; ++kb) qr[rt][kb].load(qp + off[rt] + 32 * kb, true);
 
     const bool real = lane < nv;
     gv = real ? (gv < -1024.f ? -1024.f : gv) : 0.f;   // exp is zero there; keeps -inf out of differences
@@ -175,17 +179,17 @@ __global__ __launch_bounds__(64) void delta_chunk_kernel(const DeltaParams p, bf
             }
         }
     float rk = 1.f, rq = 1.f;
-    if (p.l2norm) {
+    if (p.l2norm) {   // |k|^2 is the diagonal
 #pragma unroll
         for (int rt = 0; rt < 4; ++rt)
 #pragma unroll
             for (int r = 0; r < 4; ++r)
-                if (l == 4 * g + r) sRk[16 * rt + l] = 1.f / sqrtf(kk[rt][rt][r] + p.eps);   // the diagonal: |k|^2
+                if (l == 4 * g + r) sRk[16 * rt + l] = kk[rt][rt][r];
         wave_order();
-        rk = sRk[lane];
-    } else {
-        sRk[lane] = 1.f;
+        rk = __builtin_amdgcn_rsqf(sRk[lane] + p.eps);
+        wave_order();
     }
+    sRk[lane] = rk;
     sBk[lane] = bv * rk;
     wave_order();
 
@@ -205,22 +209,22 @@ __global__ __launch_bounds__(64) void delta_chunk_kernel(const DeltaParams p, bf
 #pragma unroll
         for (int kb = 0; kb < KB; ++kb) {
             bf16x8 a[KP];
-            qr[kb].planes(a);
+            qr[ALLQ ? rt : 0][kb].planes(a);
             if (p.l2norm)
 #pragma unroll
-                for (int e = 0; e < 8; ++e) q2 += qr[kb].get(e) * qr[kb].get(e);
+                for (int e = 0; e < 8; ++e) q2 += qr[ALLQ ? rt : 0][kb].get(e) * qr[ALLQ ? rt : 0][kb].get(e);
 #pragma unroll
             for (int ct = 0; ct <= rt; ++ct) {
                 bf16x8 j[KP];
                 kr[ct][kb].planes(j);
                 mma_planes<KP, KP, WP>(a, j, qk[ct]);
             }
-            if (rt < 3) qr[kb].load(qp + off[rt < 3 ? rt + 1 : 3] + 32 * kb, true);
+            if (!ALLQ && rt < 3) qr[0][kb].load(qp + off[rt < 3 ? rt + 1 : 3] + 32 * kb, true);
         }
         if (p.l2norm) {
             q2 += __shfl_xor(q2, 16);
             q2 += __shfl_xor(q2, 32);
-            q2 = 1.f / sqrtf(q2 + p.eps);
+            q2 = __builtin_amdgcn_rsqf(q2 + p.eps);
         } else {
             q2 = 1.f;
         }
@@ -228,7 +232,9 @@ __global__ __launch_bounds__(64) void delta_chunk_kernel(const DeltaParams p, bf
         wave_order();
         const f32x4 gh4 = *reinterpret_cast<const f32x4*>(&sGh[16 * rt + 4 * g]);
         const f32x4 gl4 = *reinterpret_cast<const f32x4*>(&sGl[16 * rt + 4 * g]);
-        const f32x4 rq4 = *reinterpret_cast<const f32x4*>(&sRq[16 * rt + 4 * g]);
+        f32x4 rq4 = *reinterpret_cast<const f32x4*>(&sRq[16 * rt + 4 * g]);
+#pragma unroll
+        for (int r = 0; r < 4; ++r) rq4[r] *= p.scale;
         const f32x4 bk4 = *reinterpret_cast<const f32x4*>(&sBk[16 * rt + 4 * g]);
 #pragma unroll
         for (int ct = 0; ct <= rt; ++ct)
@@ -238,7 +244,7 @@ __global__ __launch_bounds__(64) void delta_chunk_kernel(const DeltaParams p, bf
                 const int i = 4 * g + r;   // row in the tile
                 float D = __builtin_amdgcn_exp2f((gh4[r] - cgh[ct]) + (gl4[r] - cgl[ct])) * crk[ct];
                 if (diag && l > i) D = 0.f;
-                sM[(16 * rt + i) * LD + 16 * ct + l] = p.scale * rq4[r] * D * qk[ct][r];
+                sM[(16 * rt + i) * LD + 16 * ct + l] = rq4[r] * D * qk[ct][r];
                 // D's last use is M: kk becomes M here
                 kk[rt][ct][r] = (diag && l >= i) ? 0.f : bk4[r] * D * kk[rt][ct][r];
             }
