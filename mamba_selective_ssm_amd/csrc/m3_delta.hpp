@@ -27,7 +27,7 @@
 namespace m3 {
 
 constexpr int kDC = 64;        // tokens per chunk
-constexpr int kDScal = 6;      // per-token factor rows that the chunk kernel leaves
+constexpr int kDScal = 8;      // per-token factor rows that the chunk kernel leaves
 
 struct DeltaParams {
     const void *q, *k, *v;
@@ -67,7 +67,8 @@ struct DeltaBwdParams {
 };
 
 hipError_t launch_delta_fwd(const DeltaParams& p, int io_dtype, hipStream_t stream);
-hipError_t launch_delta_bwd(const DeltaBwdParams& p, int io_dtype, hipStream_t stream);
+hipError_t launch_delta_bwd_f32(const DeltaBwdParams& p, hipStream_t stream);
+hipError_t launch_delta_bwd_bf16(const DeltaBwdParams& p, hipStream_t stream);
 hipError_t launch_delta_step(const DeltaParams& p, int io_dtype, hipStream_t stream);
 
 constexpr bool delta_supported(int64_t N, int64_t P, int io_dtype)

@@ -338,7 +338,8 @@ m3_status m3_delta_bwd(const m3_delta_bwd_args* b, void* stream)
     const bool shared = pl.G != a->nheads;
     p.dqe = shared ? reinterpret_cast<float*>(take(pl.heads)) : b->dq;
     p.dke = shared ? reinterpret_cast<float*>(take(pl.heads)) : b->dk;
-    return status_of(m3::launch_delta_bwd(p, a->io_dtype, static_cast<hipStream_t>(stream)));
+    const hipStream_t st = static_cast<hipStream_t>(stream);
+    return status_of(a->io_dtype == M3_F32 ? m3::launch_delta_bwd_f32(p, st) : m3::launch_delta_bwd_bf16(p, st));
 }
 
 size_t m3_pool_copy_workspace_bytes(const m3_pool_copy_args* a)

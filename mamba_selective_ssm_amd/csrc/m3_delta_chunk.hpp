@@ -258,7 +258,11 @@ __global__ __launch_bounds__(64, 2) void delta_chunk_kernel(const DeltaParams p,
         sc[128 + lane] = dG * rk;
         sc[192 + lane] = p.scale * eG * rq;
         sc[256 + lane] = __builtin_amdgcn_exp2f((float)Gl);   // e^G_last, for every lane
-        if (BWD) sc[320 + lane] = rk;
+        if (BWD) {
+            sc[320 + lane] = rk;
+            sc[384 + lane] = gh;
+            sc[448 + lane] = sGl[lane];
+        }
     }
     if (!BWD)
         put_lower<AP, LD>(p.af + ci * (kTriBlocks * AP * 512), sM, l, g, lane);

@@ -68,6 +68,103 @@ template <int n> __device__ __forceinline__ void wait_loads()
     __builtin_amdgcn_s_waitcnt((n & 15) | ((n >> 4) << 14) | (7 << 4) | (15 << 8));
 }
 
+// The loader wavefront of a walk: K, the triangle `tri`, the factors and (not
+// REV) V of each chunk to LDS, NBUF - 1 steps ahead of their use.  REV: chunks
+// from the last to the first.
+template <typename IO, int N, int NS, bool REV>
+__device__ __forceinline__ void walk_loader(const DeltaParams& p, char* wlds, const bf16* tri, const DeltaRow& row, int h,
+                                            int p0, int nch, int nlast, int lane)
+{
+    using Cf = WalkCfg<IO, N, NS>;
+    constexpr int KP = Cf::KP, WP = Cf::WP, NBUF = Cf::NBUF;
+    const int rs = p.G * N, vs = p.H * p.P;
+    const int64_t ci0 = row.slot0 * p.H + h;
+    const IO* kp = reinterpret_cast<const IO*>(p.k) + (row.start * p.G + h / (p.H / p.G)) * N;
+    const IO* vp = reinterpret_cast<const IO*>(p.v) + (row.start * p.H + h) * p.P + p0;
+    // (s: step of the walk)
+    auto stage_t = [&](int s, int i0, int i1) {   // blocks i0..i1-1 of the triangle
+        const int c = REV ? nch - 1 - s : s;
+        char* dst = wlds + Cf::t + (s % Cf::TB) * Cf::tsize;
+        const char* src = reinterpret_cast<const char*>(tri + (ci0 + (int64_t)c * p.H) * (kTriBlocks * WP * 512));
+#pragma unroll
+        for (int i = 0; i < kTriBlocks * WP; ++i)
+            if (i >= i0 && i < i1) to_lds16(dst + 1024 * i, src + 1024 * i + 16 * lane);
+    };
+    auto stage = [&](int s) {
+        const int c = REV ? nch - 1 - s : s;
+        char* buf = wlds + (s % NBUF) * Cf::buf;
+        const int end = c == nch - 1 ? nlast - 1 : kDC - 1;   // last row to read
+        const IO* kc = kp + (int64_t)c * kDC * rs;
+        constexpr int RPL = 512 / N;   // K rows of one load
+        const float* fsrc = p.sc + (ci0 + (int64_t)c * p.H) * (kDScal * 64);
+        to_lds16(buf + Cf::f, fsrc + 4 * lane);
+        to_lds4(buf + Cf::f + 1024, fsrc + 256 + lane);
+        if constexpr (Cf::DIRECT) {
+#pragma unroll
+            for (int i = 0; i < 64 / RPL; ++i) {
+                const int t = RPL * i + lane / (N / 8), j = k_block<N>(t, lane % (N / 8));
+                to_lds16(buf + Cf::k + 1024 * i, kc + (t < end ? t : end) * rs + 8 * j);
+            }
+            if constexpr (!REV) {
+                const IO* vc = vp + (int64_t)c * kDC * vs;
+                constexpr int VPL = 32 / NS;   // V rows of one load
+#pragma unroll
+                for (int i = 0; i < 2 * NS; ++i) {
+                    const int t = VPL * i + lane / (2 * NS);
+                    to_lds16(buf + Cf::v + 1024 * i, vc + (t < end ? t : end) * vs + 8 * (lane % (2 * NS)));
+                }
+            }
+        } else {
+#pragma unroll 4
+            for (int i = 0; i < 64 / RPL; ++i) {
+                const int t = RPL * i + lane / (N / 8), j = k_block<N>(t, lane % (N / 8));
+                RawRow8<IO> x;
+                x.load(kc + (t < end ? t : end) * rs + 8 * j, true);
+                bf16x8 o[KP];
+                x.planes(o);
+#pragma unroll
+                for (int q = 0; q < KP; ++q)
+                    *reinterpret_cast<bf16x8*>(buf + Cf::k + q * (64 * N * 2) + 1024 * i + 16 * lane) = o[q];
+            }
+        }
+    };
+    // s_barrier alone: the release of __syncthreads would wait for every load
+    auto barrier = [&]() {
+        asm volatile("" ::: "memory");
+        __builtin_amdgcn_s_barrier();
+        asm volatile("" ::: "memory");
+    };
+#pragma unroll
+    for (int s = 0; s < NBUF - 1; ++s)
+        if (s < nch) {
+            stage(s);
+            if (s < Cf::TB) stage_t(s, 0, 3 * kTriBlocks);
+        }
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_waitcnt(0);
+    barrier();
+    for (int s = 0; s < nch; ++s) {
+        // a third of the loads beside each stage: a load takes some 30 cycles
+        // to issue, all of one chunk longer than a stage
+        const bool more = s + NBUF - 1 < nch;
+        if (more) stage(s + NBUF - 1);
+        barrier();   // R
+        if (Cf::DIRECT && more) stage_t(s + NBUF - 1, 0, 9);
+        barrier();   // U: a single T is free
+        if (Cf::DIRECT) {
+            if (more) stage_t(s + NBUF - 1, 9, 18);
+        } else if (s + 1 < nch) {
+            stage_t(s + 1, 0, 18);
+        }
+        asm volatile("" ::: "memory");
+        // the next chunk has landed
+        constexpr int loads = Cf::loads - (REV ? 2 * NS : 0);
+        if (Cf::DIRECT && NBUF == 3 && more) wait_loads<loads>();
+        else __builtin_amdgcn_s_waitcnt(0);
+        barrier();   // S
+    }
+}
+
 template <typename IO, int N, int NS, bool TRAIN>
 __global__ __launch_bounds__(64 * (6 * NS + 1)) void delta_walk_kernel(const DeltaParams p, float* Sbuf, float* Ubuf)
 {
@@ -95,85 +192,8 @@ __global__ __launch_bounds__(64 * (6 * NS + 1)) void delta_walk_kernel(const Del
     // and T's rows there are the identity's, so they write and decay nothing.
     const int nlast = (int)(row.len - (int64_t)(nch - 1) * kDC);   // tokens of the last chunk
 
-    if (wave == 6 * NS) {   // loader
-        const IO* kp = reinterpret_cast<const IO*>(p.k) + (row.start * p.G + h / (p.H / p.G)) * N;
-        const IO* vp = reinterpret_cast<const IO*>(p.v) + (row.start * p.H + h) * p.P + p0;
-        auto stage_t = [&](int c, int i0, int i1) {   // blocks i0..i1-1 of T
-            char* dst = wlds + Cf::t + (c % Cf::TB) * Cf::tsize;
-            const char* src = reinterpret_cast<const char*>(p.tf + (ci0 + (int64_t)c * p.H) * (kTriBlocks * WP * 512));
-#pragma unroll
-            for (int i = 0; i < kTriBlocks * WP; ++i)
-                if (i >= i0 && i < i1) to_lds16(dst + 1024 * i, src + 1024 * i + 16 * lane);
-        };
-        auto stage = [&](int c) {
-            char* buf = wlds + (c % NBUF) * Cf::buf;
-            const int end = c == nch - 1 ? nlast - 1 : kDC - 1;   // last row to read
-            const IO* kc = kp + (int64_t)c * kDC * rs;
-            constexpr int RPL = 512 / N;   // K rows of one load
-            const float* fsrc = p.sc + (ci0 + (int64_t)c * p.H) * (kDScal * 64);
-            to_lds16(buf + Cf::f, fsrc + 4 * lane);
-            to_lds4(buf + Cf::f + 1024, fsrc + 256 + lane);
-            if constexpr (Cf::DIRECT) {
-#pragma unroll
-                for (int i = 0; i < 64 / RPL; ++i) {
-                    const int t = RPL * i + lane / (N / 8), j = k_block<N>(t, lane % (N / 8));
-                    to_lds16(buf + Cf::k + 1024 * i, kc + (t < end ? t : end) * rs + 8 * j);
-                }
-                const IO* vc = vp + (int64_t)c * kDC * vs;
-                constexpr int VPL = 32 / NS;   // V rows of one load
-#pragma unroll
-                for (int i = 0; i < 2 * NS; ++i) {
-                    const int t = VPL * i + lane / (2 * NS);
-                    to_lds16(buf + Cf::v + 1024 * i, vc + (t < end ? t : end) * vs + 8 * (lane % (2 * NS)));
-                }
-            } else {
-#pragma unroll 4
-                for (int i = 0; i < 64 / RPL; ++i) {
-                    const int t = RPL * i + lane / (N / 8), j = k_block<N>(t, lane % (N / 8));
-                    RawRow8<IO> x;
-                    x.load(kc + (t < end ? t : end) * rs + 8 * j, true);
-                    bf16x8 o[KP];
-                    x.planes(o);
-#pragma unroll
-                    for (int q = 0; q < KP; ++q)
-                        *reinterpret_cast<bf16x8*>(buf + Cf::k + q * (64 * N * 2) + 1024 * i + 16 * lane) = o[q];
-                }
-            }
-        };
-        // s_barrier alone: the release of __syncthreads would wait for every load
-        auto barrier = [&]() {
-            asm volatile("" ::: "memory");
-            __builtin_amdgcn_s_barrier();
-            asm volatile("" ::: "memory");
-        };
-#pragma unroll
-        for (int c = 0; c < NBUF - 1; ++c)
-            if (c < nch) {
-                stage(c);
-                if (c < Cf::TB) stage_t(c, 0, 3 * kTriBlocks);
-            }
-        asm volatile("" ::: "memory");
-        __builtin_amdgcn_s_waitcnt(0);
-        barrier();
-        for (int c = 0; c < nch; ++c) {
-            // a third of the loads beside each stage: a load takes some 30
-            // cycles to issue, all of one chunk longer than a stage
-            const bool more = c + NBUF - 1 < nch;
-            if (more) stage(c + NBUF - 1);
-            barrier();   // R
-            if (Cf::DIRECT && more) stage_t(c + NBUF - 1, 0, 9);
-            barrier();   // U: a single T is free
-            if (Cf::DIRECT) {
-                if (more) stage_t(c + NBUF - 1, 9, 18);
-            } else if (c + 1 < nch) {
-                stage_t(c + 1, 0, 18);
-            }
-            asm volatile("" ::: "memory");
-            // the next chunk has landed
-            if (Cf::DIRECT && NBUF == 3 && more) wait_loads<Cf::loads>();
-            else __builtin_amdgcn_s_waitcnt(0);
-            barrier();   // S
-        }
+    if (wave == 6 * NS) {
+        walk_loader<IO, N, NS, false>(p, wlds, p.tf, row, h, p0, nch, nlast, lane);
         return;
     }
 
