@@ -316,8 +316,7 @@ __global__ __launch_bounds__(320) void delta_back_kernel(const DeltaBwdParams bp
     }
 }
 
-// Sum over the 16 lanes of one row tile's columns, over the four row groups.
-__device__ __forceinline__ float lanes_sum(float v) { return lane_group_sum<16>(v); }
+// Sum over the four lane groups (g).
 __device__ __forceinline__ float groups_sum(float v)
 {
     v += __shfl_xor(v, 16);
@@ -325,26 +324,42 @@ __device__ __forceinline__ float groups_sum(float v)
     return v;
 }
 
-// Every gradient of one chunk of one head.  Wave w has tokens 16 w .. + 15, as
-// rows of every product.  The rows of dO, dR and U are first operands as they
-// lie in memory, S0 and dS1 second operands (each value split where it is
-// used); B1 and B2 go through LDS once, because dk needs their columns.
+template <typename IO, int N, int PB> struct GradCfg {
+    static constexpr int KP = DeltaPlanes<IO>::io, WP = DeltaPlanes<IO>::wide, P = 32 * PB;
+    static constexpr int LK = N + 8, LP = P + 8, LB = 68;
+    // bytes: K, Q | one after the other: S0 and dS1 tiles (twice), U, B1 and B2 | the rest
+    static constexpr int q = KP * 64 * LK * 2, x = 2 * q, tile = WP * 16 * LP * 2, xs = 4 * tile, xu = WP * 64 * LP * 2,
+                         xb = 2 * 64 * LB * 4;
+    static constexpr int xmax = xs > xu ? (xs > xb ? xs : xb) : (xu > xb ? xu : xb);
+    static constexpr int f = x + xmax, total = f + (9 * 64 + 4 * 64 + 64 + 64 + 4) * 4;
+};
+
+// Every gradient of one chunk of one head.  Wave w has tokens 16 w .. + 15:
+// every product is made as its transpose, so that a lane has one token (l) and
+// its row's factors and sums are scalars of the lane, and results leave as four
+// neighbours.  The rows of dO, dR and U are second operands as they lie in
+// memory; S0 and dS1 go through LDS in tiles of 16 rows, split once for all
+// four waves, the next tile's loads in flight; then U takes that place, then
+// B1 and B2, whose columns dk needs.  About 250 products of 16x16x32 and as
+// many bytes as a chunk's two states and its rows, read once.
 template <typename IO, int N, int PB>
-__global__ __launch_bounds__(256) void delta_grad_kernel(const DeltaBwdParams bp)
+__global__ __launch_bounds__(256, PB <= 2 ? 2 : 1) void delta_grad_kernel(const DeltaBwdParams bp)
 {
+    using Cf = GradCfg<IO, N, PB>;
     const DeltaParams& p = bp.f;
-    constexpr int KP = DeltaPlanes<IO>::io, WP = DeltaPlanes<IO>::wide, NT = N / 16, LK = N + 8, LB = 68, P = 32 * PB;
+    constexpr int KP = Cf::KP, WP = Cf::WP, NT = N / 16, LK = Cf::LK, LP = Cf::LP, LB = Cf::LB, P = Cf::P;
     extern __shared__ __attribute__((aligned(16))) char glds[];
     bf16* sK = reinterpret_cast<bf16*>(glds);
-    bf16* sQ = sK + KP * 64 * LK;
-    float* sB1 = reinterpret_cast<float*>(sQ + KP * 64 * LK);
+    bf16* sQ = reinterpret_cast<bf16*>(glds + Cf::q);
+    bf16* sX = reinterpret_cast<bf16*>(glds + Cf::x);
+    float* sB1 = reinterpret_cast<float*>(glds + Cf::x);
     float* sB2 = sB1 + 64 * LB;
-    float* sCol = sB2 + 64 * LB;    // [4][64] column sums of each wave's rows
-    float* sG = sCol + 256;         // [64] dG but for the column sums and the total
-    float* sUs = sG + 64;           // [64] what the factor d adds to G_last and takes from G
-    float* sDb = sUs + 64;          // [64] dR.V
-    float* sF = sDb + 64;           // [8][64] factors and [64] 1/|q|
-    float* sTot = sF + 9 * 64;      // [4] each wave's share of <S0, dS1>
+    float* sF = reinterpret_cast<float*>(glds + Cf::f);   // [8][64] factors, [64] 1/|q|
+    float* sRq = sF + 8 * 64;
+    float* sCol = sRq + 64;    // [4][64] column sums of each wave's rows
+    float* sG = sCol + 256;    // [64] dG but for the column sums and the total
+    float* sUs = sG + 64;      // [64] what the factor d adds to G_last and takes from G
+    float* sTot = sUs + 64;    // [4] each wave's share of <S0, dS1>
     const int tid = threadIdx.x, lane = tid & 63, l = lane & 15, g = lane >> 4;
     const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int64_t bid = blockIdx.x;
@@ -360,63 +375,102 @@ __global__ __launch_bounds__(256) void delta_grad_kernel(const DeltaBwdParams bp
     const IO* op = reinterpret_cast<const IO*>(bp.dout) + (t0 * p.H + h) * P;
     const IO* vp = reinterpret_cast<const IO*>(p.v) + (t0 * p.H + h) * P;
     const int rs = p.G * N, vs = p.H * P;
-
-    // K, Q to LDS, rows past the end zero
-    for (int i = tid; i < 64 * N / 8; i += 256) {
-        const int t = i / (N / 8), j = i % (N / 8);
-        RawRow8<IO> x, y;
-        x.load(kp + (t < nv ? t : 0) * rs + 8 * j, t < nv);
-        y.load(qp + (t < nv ? t : 0) * rs + 8 * j, t < nv);
-        bf16x8 o[KP];
-        x.planes(o);
-#pragma unroll
-        for (int e = 0; e < KP; ++e) *reinterpret_cast<bf16x8*>(sK + (e * 64 + t) * LK + 8 * j) = o[e];
-        y.planes(o);
-#pragma unroll
-        for (int e = 0; e < KP; ++e) *reinterpret_cast<bf16x8*>(sQ + (e * 64 + t) * LK + 8 * j) = o[e];
-    }
-    const float* sc = p.sc + ci * (kDScal * 64);
-    for (int i = tid; i < kDScal * 64; i += 256) sF[i] = sc[i];
     const f32x4 fz = {0.f, 0.f, 0.f, 0.f};
 
-    // first operands: rows of dO, dR, U; dv, and dR.V for dbeta
-    const int irow = 16 * w + l, drow = 16 * w + 4 * g;
+    // the tiles of S0 and dS1: this thread's four values of each, SI times
+    constexpr int SI = (16 * P / 4 + 255) / 256;
+    const float* Sb = bp.S + ci * N * (int64_t)P;
+    const float* Db = bp.dS + ci * N * (int64_t)P;
+    f32x4 sr[SI], dr[SI];
+    auto load_tile = [&](int nt) {
+#pragma unroll
+        for (int i = 0; i < SI; ++i) {
+            int j = tid + 256 * i;
+            if (16 * P / 4 % 256 != 0 && j >= 16 * P / 4) j = 0;   // (stored by thread 0 alone)
+            sr[i] = *reinterpret_cast<const f32x4*>(Sb + nt * 16 * P + 4 * j);
+            dr[i] = *reinterpret_cast<const f32x4*>(Db + nt * 16 * P + 4 * j);
+        }
+    };
+    float tot = 0.f;
+    auto put_tile = [&](int nt) {
+        bf16* s = sX + (nt & 1) * (Cf::tile);   // (two tiles of `tile` bytes each)
+#pragma unroll
+        for (int i = 0; i < SI; ++i) {
+            const int j = tid + 256 * i;
+            if (16 * P / 4 % 256 != 0 && j >= 16 * P / 4) continue;
+            const int r = j / (P / 4), x = j % (P / 4);
+            bf16x4 o[WP];
+            to_planes4<WP>(sr[i], o);
+#pragma unroll
+            for (int e = 0; e < WP; ++e) *reinterpret_cast<bf16x4*>(s + (e * 16 + r) * LP + 4 * x) = o[e];
+            to_planes4<WP>(dr[i], o);
+#pragma unroll
+            for (int e = 0; e < WP; ++e) *reinterpret_cast<bf16x4*>(s + Cf::tile / 2 + (e * 16 + r) * LP + 4 * x) = o[e];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) tot += sr[i][e] * dr[i][e];
+        }
+    };
+    load_tile(0);
+
+    // second operands: rows of dO, dR, U; dv, and dR.V for dbeta
+    const int irow = 16 * w + l;   // this lane's token
     const bool real = irow < nv;
     bf16x8 o8[PB][KP], r8[PB][WP], u8[PB][WP];
     float drv = 0.f;
     const float* Ub = bp.U + ci * 64 * (int64_t)P;
     const float* Rb = bp.dR + ci * 64 * (int64_t)P;
-    const float bi = sc[irow];
+    const float* sc = p.sc + ci * (kDScal * 64);
+    const float beta = sc[irow];
+    {
+        RawRow8<IO> x[PB], v[PB];
+        RawRow8<float> r[PB], u[PB];
 #pragma unroll
-    for (int kb = 0; kb < PB; ++kb) {
-        const int pc = 32 * kb + 8 * g;
-        RawRow8<IO> x, v;
-        RawRow8<float> r, u;
-        x.load(op + (real ? irow : 0) * vs + pc, real);
-        v.load(vp + (real ? irow : 0) * vs + pc, real);
-        r.load(Rb + irow * P + pc, true);
-        u.load(Ub + irow * P + pc, true);
-        x.planes(o8[kb]);
-        r.planes(r8[kb]);
-        u.planes(u8[kb]);
-        f32x4 d0, d1;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            drv += r.get(e) * v.get(e);
-            if (e < 4) d0[e] = bi * r.get(e);
-            else d1[e - 4] = bi * r.get(e);
+        for (int kb = 0; kb < PB; ++kb) {
+            const int pc = 32 * kb + 8 * g;
+            x[kb].load(op + (real ? irow : 0) * vs + pc, real);
+            v[kb].load(vp + (real ? irow : 0) * vs + pc, real);
+            r[kb].load(Rb + irow * P + pc, true);
+            u[kb].load(Ub + irow * P + pc, true);
         }
-        if (real) {
-            float* dv = bp.dv + ((t0 + irow) * p.H + h) * P + pc;
-            *reinterpret_cast<f32x4*>(dv) = d0;
-            *reinterpret_cast<f32x4*>(dv + 4) = d1;
+        // K, Q to LDS, rows past the end zero
+        for (int i = tid; i < 64 * N / 8; i += 256) {
+            const int t = i / (N / 8), j = i % (N / 8);
+            RawRow8<IO> y, z;
+            y.load(kp + (t < nv ? t : 0) * rs + 8 * j, t < nv);
+            z.load(qp + (t < nv ? t : 0) * rs + 8 * j, t < nv);
+            bf16x8 o[KP];
+            y.planes(o);
+#pragma unroll
+            for (int e = 0; e < KP; ++e) *reinterpret_cast<bf16x8*>(sK + (e * 64 + t) * LK + 8 * j) = o[e];
+            z.planes(o);
+#pragma unroll
+            for (int e = 0; e < KP; ++e) *reinterpret_cast<bf16x8*>(sQ + (e * 64 + t) * LK + 8 * j) = o[e];
+        }
+        for (int i = tid; i < kDScal * 64; i += 256) sF[i] = sc[i];
+        put_tile(0);
+#pragma unroll
+        for (int kb = 0; kb < PB; ++kb) {
+            x[kb].planes(o8[kb]);
+            r[kb].planes(r8[kb]);
+            u[kb].planes(u8[kb]);
+            f32x4 d0, d1;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                drv += r[kb].get(e) * v[kb].get(e);
+                if (e < 4) d0[e] = beta * r[kb].get(e);
+                else d1[e - 4] = beta * r[kb].get(e);
+            }
+            if (real) {
+                float* dv = bp.dv + ((t0 + irow) * p.H + h) * P + 32 * kb + 8 * g;
+                *reinterpret_cast<f32x4*>(dv) = d0;
+                *reinterpret_cast<f32x4*>(dv + 4) = d1;
+            }
         }
     }
-    drv = groups_sum(drv);   // of token irow
-    if (g == 0) sDb[irow] = drv;
+    drv = groups_sum(drv);
     __syncthreads();
 
-    // 1/|q| of the wave's tokens
+    // this token's factors
     float q2 = 0.f;
 #pragma unroll
     for (int j = 0; j < N / 32; ++j)
@@ -428,25 +482,80 @@ __global__ __launch_bounds__(256) void delta_grad_kernel(const DeltaBwdParams bp
             q2 += x * x;
         }
     q2 = groups_sum(q2);
-    float* sRq = sF + kDScal * 64;
-    if (g == 0) sRq[irow] = !real ? 0.f : p.l2norm ? __builtin_amdgcn_rsqf(q2 + p.eps) : 1.f;
-    wave_order();
-    const f32x4 beta4 = *reinterpret_cast<const f32x4*>(sF + drow);
-    const f32x4 rk4 = *reinterpret_cast<const f32x4*>(sF + 320 + drow), rq4 = *reinterpret_cast<const f32x4*>(sRq + drow);
-    const f32x4 gh4 = *reinterpret_cast<const f32x4*>(sF + 384 + drow), gl4 = *reinterpret_cast<const f32x4*>(sF + 448 + drow);
+    const float rq = !real ? 0.f : p.l2norm ? __builtin_amdgcn_rsqf(q2 + p.eps) : 1.f;
+    if (g == 0) sRq[irow] = rq;   // (read after the next barriers)
+    const float rk = sF[320 + irow], gh = sF[384 + irow], gl = sF[448 + irow];
+    const float eG = __builtin_amdgcn_exp2f(gh + gl);
+    const float dG = __builtin_amdgcn_exp2f((sF[384 + 63] - gh) + (sF[448 + 63] - gl));
 
-    f32x4 e4, d4;   // e^G, e^(G_last - G)
+    // dO S0^T, dR S0^T, U dS1^T: rows 16 nt + 4 g + r of their transposes
+    f32x4 accq[NT], acck[NT];
+    float qs = 0.f, ks = 0.f, us = 0.f;
+    // four values of this token's unit row, columns 16 nt + 4 g ..
+    auto row4 = [&](const bf16* s, int nt, float scale) {
+        f32x4 x = fz;
 #pragma unroll
-    for (int r = 0; r < 4; ++r) {
-        e4[r] = __builtin_amdgcn_exp2f(gh4[r] + gl4[r]);
-        d4[r] = __builtin_amdgcn_exp2f((sF[384 + 63] - gh4[r]) + (sF[448 + 63] - gl4[r]));
+        for (int e = KP - 1; e >= 0; --e) {
+            const bf16x4 y = *reinterpret_cast<const bf16x4*>(s + (e * 64 + irow) * LK + 16 * nt + 4 * g);
+#pragma unroll
+            for (int r = 0; r < 4; ++r) x[r] += (float)y[r];
+        }
+#pragma unroll
+        for (int r = 0; r < 4; ++r) x[r] *= scale;
+        return x;
+    };
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+        if (nt + 1 < NT) load_tile(nt + 1);
+        const bf16* s = sX + (nt & 1) * Cf::tile + l * LP + 8 * g;
+        f32x4 w1 = fz, w2 = fz, w3 = fz;
+#pragma unroll
+        for (int kb = 0; kb < PB; ++kb) {
+            bf16x8 s8[WP], d8[WP];
+#pragma unroll
+            for (int e = 0; e < WP; ++e) {
+                s8[e] = *reinterpret_cast<const bf16x8*>(s + e * 16 * LP + 32 * kb);
+                d8[e] = *reinterpret_cast<const bf16x8*>(s + Cf::tile / 2 + e * 16 * LP + 32 * kb);
+            }
+            mma_planes<WP, KP, WP>(s8, o8[kb], w1);
+            mma_planes<WP, WP, WP>(s8, r8[kb], w2);
+            mma_planes<WP, WP, WP>(d8, u8[kb], w3);
+        }
+        const f32x4 qv = row4(sQ, nt, rq), kv = row4(sK, nt, rk);
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+            const float x = p.scale * eG * w1[r], y = eG * w2[r], z = dG * w3[r];
+            qs += qv[r] * x;
+            ks += kv[r] * y;
+            us += kv[r] * z;
+            accq[nt][r] = x;
+            acck[nt][r] = z - beta * y;
+        }
+        if (nt + 1 < NT) put_tile(nt + 1);
+        __syncthreads();
     }
+    qs = groups_sum(qs);
+    ks = groups_sum(ks);
+    us = groups_sum(us);
+    tot = groups_sum(lane_group_sum<16>(tot));
+    if (lane == 0) sTot[w] = tot;
 
-    // B1, B2, the row and column sums of Z = B1 (q.k) + B2 (k.k), and the M part of dbeta
-    f32x4 zrow = fz, mrow = fz;
+    // U's planes where the tiles were
+#pragma unroll
+    for (int kb = 0; kb < PB; ++kb)
+#pragma unroll
+        for (int e = 0; e < WP; ++e) *reinterpret_cast<bf16x8*>(sX + (e * 64 + irow) * LP + 32 * kb + 8 * g) = u8[kb][e];
+    __syncthreads();
+
+    // B1, B2 (this token's row, keys 16 ct + 4 g + r), the row and column sums
+    // of Z = B1 (q.k) + B2 (k.k), and the M part of dbeta
+    float zrow = 0.f, mrow = 0.f;
+    f32x4 v1[4], v2[4];
 #pragma unroll
     for (int ct = 0; ct < 4; ++ct) {
-        float zc = 0.f;
+        f32x4 zc = fz;
+        v1[ct] = fz;
+        v2[ct] = fz;
         if (ct <= w) {   // wave-uniform
             f32x4 qk = fz, kk = fz, dA = fz, dM = fz;
 #pragma unroll
@@ -458,188 +567,131 @@ __global__ __launch_bounds__(256) void delta_grad_kernel(const DeltaBwdParams bp
                     q[e] = *reinterpret_cast<const bf16x8*>(sQ + (e * 64 + irow) * LK + 32 * kb + 8 * g);
                     j[e] = *reinterpret_cast<const bf16x8*>(sK + (e * 64 + 16 * ct + l) * LK + 32 * kb + 8 * g);
                 }
-                mma_planes<KP, KP, WP>(a, j, kk);
-                mma_planes<KP, KP, WP>(q, j, qk);
+                mma_planes<KP, KP, WP>(j, a, kk);
+                mma_planes<KP, KP, WP>(j, q, qk);
             }
 #pragma unroll
             for (int kb = 0; kb < PB; ++kb) {
-                RawRow8<float> u;
-                u.load(Ub + (16 * ct + l) * P + 32 * kb + 8 * g, true);
                 bf16x8 j[WP];
-                u.planes(j);
-                mma_planes<KP, WP, WP>(o8[kb], j, dA);
-                mma_planes<WP, WP, WP>(r8[kb], j, dM);
+#pragma unroll
+                for (int e = 0; e < WP; ++e)
+                    j[e] = *reinterpret_cast<const bf16x8*>(sX + (e * 64 + 16 * ct + l) * LP + 32 * kb + 8 * g);
+                mma_planes<WP, KP, WP>(j, o8[kb], dA);
+                mma_planes<WP, WP, WP>(j, r8[kb], dM);
             }
-            const int j = 16 * ct + l;
-            const float gh = sF[384 + j], gl = sF[448 + j], rkj = sF[320 + j];
+            const int j0 = 16 * ct + 4 * g;
+            const f32x4 rk4 = *reinterpret_cast<const f32x4*>(sF + 320 + j0);
+            const f32x4 gh4 = *reinterpret_cast<const f32x4*>(sF + 384 + j0);
+            const f32x4 gl4 = *reinterpret_cast<const f32x4*>(sF + 448 + j0);
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
-                const bool diag = ct == w;
-                const int i = 4 * g + r;
-                float D = __builtin_amdgcn_exp2f((gh4[r] - gh) + (gl4[r] - gl));
-                if (diag && l > i) D = 0.f;
-                const float dm = (diag && l >= i) ? 0.f : -D * dM[r];
-                const float b1 = p.scale * D * dA[r], kn = rk4[r] * rkj * kk[r], b2 = beta4[r] * dm;
-                const float z = b1 * (rq4[r] * rkj * qk[r]) + b2 * kn;
-                zrow[r] += z;
-                mrow[r] += dm * kn;
-                zc += z;
-                sB1[(16 * w + i) * LB + j] = b1;
-                sB2[(16 * w + i) * LB + j] = b2;
+                float D = __builtin_amdgcn_exp2f((gh - gh4[r]) + (gl - gl4[r]));
+                if (ct == w && 4 * g + r > l) D = 0.f;
+                const float dm = (ct == w && 4 * g + r >= l) ? 0.f : -D * dM[r];
+                const float b1 = p.scale * D * dA[r], kn = rk * rk4[r] * kk[r], b2 = beta * dm;
+                const float z = b1 * (rq * rk4[r] * qk[r]) + b2 * kn;
+                zrow += z;
+                mrow += dm * kn;
+                zc[r] = z;
+                v1[ct][r] = b1;
+                v2[ct][r] = b2;
             }
         }
-        zc = groups_sum(zc);
-        if (g == 0) sCol[w * 64 + 16 * ct + l] = zc;
-    }
 #pragma unroll
-    for (int r = 0; r < 4; ++r) {
-        zrow[r] = lanes_sum(zrow[r]);
-        mrow[r] = lanes_sum(mrow[r]);
+        for (int r = 0; r < 4; ++r) zc[r] = lane_group_sum<16>(zc[r]);
+        if (l == 0) *reinterpret_cast<f32x4*>(sCol + w * 64 + 16 * ct + 4 * g) = zc;
+    }
+    zrow = groups_sum(zrow);
+    mrow = groups_sum(mrow);
+    __syncthreads();
+#pragma unroll
+    for (int ct = 0; ct < 4; ++ct) {
+        *reinterpret_cast<f32x4*>(sB1 + irow * LB + 16 * ct + 4 * g) = v1[ct];
+        *reinterpret_cast<f32x4*>(sB2 + irow * LB + 16 * ct + 4 * g) = v2[ct];
+    }
+    // dbeta and dG of this token
+    if (g == 0) {
+        sG[irow] = qs - beta * ks + zrow - us;
+        sUs[irow] = us;
+        if (real) bp.dbeta[(t0 + irow) * p.H + h] = drv - ks + mrow;
     }
     __syncthreads();
 
-    // first operands from B1 (rows: dq; columns: dk) and B2 + B2^T (dk), with
-    // the unit factors of the second operands' rows
-    bf16x8 b1[2][WP], b1t[2][WP], b2[2][WP];
+    // second operands from B1 (rows: dq; columns: dk) and B2 + B2^T (dk), with
+    // the unit factors of the first operands' rows; zero off their triangles
 #pragma unroll
     for (int kb = 0; kb < 2; ++kb) {
-        float x[8], y[8], z[8];
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            const int j = 32 * kb + 8 * g + e;
-            const float rkj = sF[320 + j], rqj = sRq[j];
-            x[e] = j <= irow ? sB1[irow * LB + j] * rkj : 0.f;
-            y[e] = j >= irow ? sB1[j * LB + irow] * rqj : 0.f;
-            z[e] = (j < irow ? sB2[irow * LB + j] : j > irow ? sB2[j * LB + irow] : 0.f) * rkj;
-        }
+        bf16x8 b1[WP], b1t[WP], b2[WP];
+        const int j0 = 32 * kb + 8 * g;
 #pragma unroll
         for (int e = 0; e < 8; e += 2) {
-            bf16x2 t[WP];
-            to_planes2<WP>(x[e], x[e + 1], t);
+            float x[2], y[2], z[2];
 #pragma unroll
-            for (int i = 0; i < WP; ++i) { b1[kb][i][e] = t[i][0]; b1[kb][i][e + 1] = t[i][1]; }
-            to_planes2<WP>(y[e], y[e + 1], t);
-#pragma unroll
-            for (int i = 0; i < WP; ++i) { b1t[kb][i][e] = t[i][0]; b1t[kb][i][e + 1] = t[i][1]; }
-            to_planes2<WP>(z[e], z[e + 1], t);
-#pragma unroll
-            for (int i = 0; i < WP; ++i) { b2[kb][i][e] = t[i][0]; b2[kb][i][e + 1] = t[i][1]; }
-        }
-    }
-
-    // column tiles of dq and dk
-    f32x4 accq[NT], acck[NT], qs = fz, ks = fz, us = fz, qd = fz, kd = fz;
-    float tot = 0.f;
-    const float* Sb = bp.S + ci * N * (int64_t)P;
-    const float* Db = bp.dS + ci * N * (int64_t)P;
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-        f32x4 w1 = fz, w2 = fz, w3 = fz;
-#pragma unroll
-        for (int kb = 0; kb < PB; ++kb) {
-            RawRow8<float> s, d;
-            s.load(Sb + (16 * nt + l) * P + 32 * kb + 8 * g, true);
-            d.load(Db + (16 * nt + l) * P + 32 * kb + 8 * g, true);
-            bf16x8 s8[WP], d8[WP];
-            s.planes(s8);
-            d.planes(d8);
-            mma_planes<KP, WP, WP>(o8[kb], s8, w1);
-            mma_planes<WP, WP, WP>(r8[kb], s8, w2);
-            mma_planes<WP, WP, WP>(u8[kb], d8, w3);
-            if ((nt & 3) == w)
-#pragma unroll
-                for (int e = 0; e < 8; ++e) tot += s.get(e) * d.get(e);
-        }
-        // this tile's values of q and k at the result's places (unit rows)
-        f32x4 qv = fz, kv = fz;
-#pragma unroll
-        for (int e = KP - 1; e >= 0; --e) {
-            const int at = (e * 64 + 16 * w + 4 * g + (l >> 2)) * LK + 16 * nt + 4 * (l & 3);
-            const bf16x4 x = lds_read_tr4(sQ + at), y = lds_read_tr4(sK + at);
-#pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                qv[r] += (float)x[r];
-                kv[r] += (float)y[r];
+            for (int i = 0; i < 2; ++i) {
+                const int j = j0 + e + i;
+                const float rkj = sF[320 + j];
+                x[i] = sB1[irow * LB + j] * rkj;
+                y[i] = sB1[j * LB + irow] * sRq[j];
+                z[i] = (sB2[irow * LB + j] + sB2[j * LB + irow]) * rkj;
             }
+            bf16x2 t[WP];
+            to_planes2<WP>(x[0], x[1], t);
+#pragma unroll
+            for (int i = 0; i < WP; ++i) { b1[i][e] = t[i][0]; b1[i][e + 1] = t[i][1]; }
+            to_planes2<WP>(y[0], y[1], t);
+#pragma unroll
+            for (int i = 0; i < WP; ++i) { b1t[i][e] = t[i][0]; b1t[i][e + 1] = t[i][1]; }
+            to_planes2<WP>(z[0], z[1], t);
+#pragma unroll
+            for (int i = 0; i < WP; ++i) { b2[i][e] = t[i][0]; b2[i][e + 1] = t[i][1]; }
         }
 #pragma unroll
-        for (int r = 0; r < 4; ++r) {
-            qv[r] *= rq4[r];
-            kv[r] *= rk4[r];
-            w1[r] *= p.scale * e4[r];
-            w2[r] *= e4[r];
-            w3[r] *= d4[r];
-            qs[r] += qv[r] * w1[r];
-            ks[r] += kv[r] * w2[r];
-            us[r] += kv[r] * w3[r];
-            accq[nt][r] = w1[r];
-            acck[nt][r] = w3[r] - beta4[r] * w2[r];
-        }
-#pragma unroll
-        for (int kb = 0; kb < 2; ++kb) {
+        for (int nt = 0; nt < NT; ++nt) {
             bf16x8 kt[KP], qt[KP];
 #pragma unroll
             for (int e = 0; e < KP; ++e) {
-                const int at = (e * 64 + 32 * kb + 8 * g + (l >> 2)) * LK + 16 * nt + 4 * (l & 3);
+                const int at = (e * 64 + j0 + (l >> 2)) * LK + 16 * nt + 4 * (l & 3);
                 kt[e] = join8(lds_read_tr4(sK + at), lds_read_tr4(sK + at + 4 * LK));
                 qt[e] = join8(lds_read_tr4(sQ + at), lds_read_tr4(sQ + at + 4 * LK));
             }
-            mma_planes<WP, KP, WP>(b1[kb], kt, accq[nt]);
-            mma_planes<WP, KP, WP>(b1t[kb], qt, acck[nt]);
-            mma_planes<WP, KP, WP>(b2[kb], kt, acck[nt]);
-        }
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-            qd[r] += qv[r] * accq[nt][r];
-            kd[r] += kv[r] * acck[nt][r];
+            mma_planes<KP, WP, WP>(kt, b1, accq[nt]);
+            mma_planes<KP, WP, WP>(qt, b1t, acck[nt]);
+            mma_planes<KP, WP, WP>(kt, b2, acck[nt]);
         }
     }
-    // row sums over the tokens' columns
-#pragma unroll
-    for (int r = 0; r < 4; ++r) {
-        qs[r] = lanes_sum(qs[r]);
-        ks[r] = lanes_sum(ks[r]);
-        us[r] = lanes_sum(us[r]);
-        qd[r] = lanes_sum(qd[r]);
-        kd[r] = lanes_sum(kd[r]);
-    }
-    tot = groups_sum(lanes_sum(tot));
-    if (lane == 0) sTot[w] = tot;
 
     // dq, dk through the unit rows: r (d - x (x.d))
+    float qd = 0.f, kd = 0.f;
+    if (p.l2norm) {
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
+        for (int nt = 0; nt < NT; ++nt) {
+            const f32x4 qv = row4(sQ, nt, rq), kv = row4(sK, nt, rk);
 #pragma unroll
-        for (int r = 0; r < 4; ++r) {
-            const int t = drow + r;
-            if (t >= nv) continue;
-            float dq = accq[nt][r], dk = acck[nt][r];
-            if (p.l2norm) {
-                float x = 0.f, y = 0.f;
-#pragma unroll
-                for (int e = KP - 1; e >= 0; --e) {
-                    x += (float)sQ[(e * 64 + t) * LK + 16 * nt + l];
-                    y += (float)sK[(e * 64 + t) * LK + 16 * nt + l];
-                }
-                dq = rq4[r] * (dq - x * rq4[r] * qd[r]);
-                dk = rk4[r] * (dk - y * rk4[r] * kd[r]);
+            for (int r = 0; r < 4; ++r) {
+                qd += qv[r] * accq[nt][r];
+                kd += kv[r] * acck[nt][r];
             }
-            const int64_t at = ((t0 + t) * p.H + h) * N + 16 * nt + l;
-            bp.dqe[at] = dq;
-            bp.dke[at] = dk;
         }
+        qd = groups_sum(qd);
+        kd = groups_sum(kd);
     }
-    // dbeta and dG of this wave's tokens
-    if (l == 0) {
+    if (real) {
+        const int64_t at = ((t0 + irow) * p.H + h) * N + 4 * g;
 #pragma unroll
-        for (int r = 0; r < 4; ++r) {
-            const int t = drow + r;
-            sG[t] = qs[r] - beta4[r] * ks[r] + zrow[r] - us[r];
-            sUs[t] = us[r];
-            if (t < nv) bp.dbeta[(t0 + t) * p.H + h] = sDb[t] - ks[r] + mrow[r];
+        for (int nt = 0; nt < NT; ++nt) {
+            f32x4 dq = accq[nt], dk = acck[nt];
+            if (p.l2norm) {
+                const f32x4 qv = row4(sQ, nt, rq), kv = row4(sK, nt, rk);
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    dq[r] = rq * (dq[r] - qv[r] * qd);
+                    dk[r] = rk * (dk[r] - kv[r] * kd);
+                }
+            }
+            *reinterpret_cast<f32x4*>(bp.dqe + at + 16 * nt) = dq;
+            *reinterpret_cast<f32x4*>(bp.dke + at + 16 * nt) = dk;
         }
     }
-    __syncthreads();
     if (w == 0) {
         double x = (double)sG[lane] - ((double)sCol[lane] + sCol[64 + lane] + sCol[128 + lane] + sCol[192 + lane]);
         const double u = wave_inclusive_sum_d((double)sUs[lane]);
@@ -685,15 +737,11 @@ static __global__ __launch_bounds__(256) void delta_rest_kernel(const DeltaParam
     }
 }
 
-template <typename IO, int N> struct GradLds {
-    static constexpr size_t bytes = 2 * (size_t)DeltaPlanes<IO>::io * 64 * (N + 8) * 2 + (2 * 64 * 68 + 256 + 3 * 64 + 9 * 64 + 4) * 4;
-};
-
 template <typename IO, int N, int PB>
 hipError_t launch_delta_grad(const DeltaBwdParams& bp, hipStream_t stream)
 {
     auto* const kern = &delta_grad_kernel<IO, N, PB>;
-    constexpr size_t lds = GradLds<IO, N>::bytes;
+    constexpr size_t lds = GradCfg<IO, N, PB>::total;
     static_assert(lds <= 160 * 1024, "a workgroup's LDS");
     static const hipError_t attr = delta_allow_lds(kern, lds);
     if (attr != hipSuccess) return attr;
