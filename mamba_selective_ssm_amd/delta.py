@@ -20,11 +20,12 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
+import struct
 from typing import NamedTuple, Optional
 
 import torch
 
-from .binding import M3Error, _check, _io_code, _ptr, load_library
+from .binding import M3Error, _check, _io_code, load_library
 
 _vp, _i64, _i32, _f32 = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32, ctypes.c_float
 
@@ -62,82 +63,94 @@ class DeltaGrads(NamedTuple):
     dh_in: Optional[torch.Tensor]
 
 
-@contextlib.contextmanager
-def on_device_of(t: torch.Tensor, stream=None):
-    """The tensor's device made current, and `stream` (None: that device's
-    current stream) the stream that the call's own allocations belong to.
-    Yields the stream's handle."""
-    with torch.cuda.device(t.device):
-        if stream is None:
-            yield torch.cuda.current_stream().cuda_stream
-        else:
-            if stream.device != t.device:
-                raise ValueError("stream belongs to %s, the tensors to %s" % (stream.device, t.device))
-            with torch.cuda.stream(stream):
-                yield stream.cuda_stream
+def packer(cls):
+    """A function from all of a structure's values, in their order, to its
+    bytes: a call costs one of these instead of an attribute store per field."""
+    codes = {_i64: "q", _i32: "i", _f32: "f", _vp: "P", ctypes.c_size_t: "N"}
+
+    def fmt(c):
+        return "".join(fmt(f) if isinstance(f, type) and issubclass(f, ctypes.Structure) else
+                       codes[f._type_] * f._length_ if hasattr(f, "_length_") else codes[f] for _, f in c._fields_)
+
+    s = struct.Struct("@" + fmt(cls))
+    assert s.size == ctypes.sizeof(cls), cls
+    return s.pack
 
 
-def same_device(t: torch.Tensor, name: str, device):
-    if t.device != device:
-        raise ValueError("%s is on %s, q on %s" % (name, t.device, device))
+_pack_fwd, _pack_step, _pack_bwd = packer(DeltaArgs), packer(DeltaStepArgs), packer(DeltaBwdArgs)
+
+
+def enter(device, stream):
+    """The handle of the stream that a call on `device` runs on (None: the
+    device's current stream), and the contexts that make that device and
+    stream current, which the call's own allocations follow (None: they are)."""
+    here = torch.cuda.current_device()
+    if stream is None and here == device.index:
+        return torch.cuda.current_stream().cuda_stream, None
+    ctx = contextlib.ExitStack()
+    ctx.enter_context(torch.cuda.device(device))
+    if stream is None:
+        return torch.cuda.current_stream().cuda_stream, ctx
+    if stream.device != device:
+        ctx.close()
+        raise ValueError("stream belongs to %s, the tensors to %s" % (stream.device, device))
+    ctx.enter_context(torch.cuda.stream(stream))
+    return stream.cuda_stream, ctx
+
+
+def expect(t: torch.Tensor, name: str, shape, dtype, device):
+    """_check, and the device that all of a call's tensors share."""
+    if t.shape != shape or t.dtype is not dtype or t.device != device or not t.is_contiguous():
+        _check(t, name, shape, dtype)
+        raise ValueError("%s is on %s, not on %s" % (name, t.device, device))
 
 
 def _shapes(q, k, v, g, beta, step):
-    """(Bx, L, H, G, N, P) after the checks of the token arrays."""
+    """(token dimensions, H, G, N, P, io code, device) after the checks of the token arrays."""
     lead = 1 if step else 2
     if q.dim() != lead + 2 or v.dim() != lead + 2:
         raise ValueError("q and v: expected %d dimensions, got %d and %d" % (lead + 2, q.dim(), v.dim()))
-    tok, (G, N), (H, P) = tuple(q.shape[:lead]), q.shape[lead:], v.shape[lead:]
-    _io_code(q.dtype)
-    for t, name, shape, dt in ((q, "q", tok + (G, N), q.dtype), (k, "k", tok + (G, N), q.dtype),
-                               (v, "v", tok + (H, P), q.dtype), (g, "g", tok + (H,), torch.float32),
-                               (beta, "beta", tok + (H,), torch.float32)):
-        _check(t, name, shape, dt)
-        same_device(t, name, q.device)
+    sq, sv, dt, dev = tuple(q.shape), tuple(v.shape), q.dtype, q.device
+    tok, (G, N), (H, P) = sq[:lead], sq[lead:], sv[lead:]
+    io = _io_code(dt)
+    if dev.type != "cuda":
+        raise ValueError("q must be a device tensor")
+    expect(q, "q", sq, dt, dev)
+    expect(k, "k", sq, dt, dev)
+    expect(v, "v", tok + (H, P), dt, dev)
+    expect(g, "g", tok + (H,), torch.float32, dev)
+    expect(beta, "beta", tok + (H,), torch.float32, dev)
     if G < 1 or H % G != 0:
         raise ValueError("heads (%d) must be a multiple of q and k's groups (%d)" % (H, G))
-    return tok[0], (1 if step else tok[1]), H, G, N, P
+    return tok, H, G, N, P, io, dev
 
 
-def _common(a, H, G, N, P, io, scale, l2norm, norm_eps):
-    a.nheads, a.ngroups, a.headdim, a.dstate, a.io_dtype = H, G, P, N, io
-    a.scale = float(N ** -0.5 if scale is None else scale)
-    a.l2norm, a.norm_eps = int(bool(l2norm)), float(norm_eps)
-
-
-def _rows(a, cu_seqlens, max_seqlen, Bx, L, device):
-    """Batch rows or packed sequences of the call."""
+def _rows(cu_seqlens, max_seqlen, tok, dev):
+    """(batch rows or packed sequences, offsets' address, longest) of a call."""
     if cu_seqlens is None:
-        a.batch, a.seqlen = Bx, L
-        return Bx
-    if Bx != 1:
+        return tok[0], 0, 0
+    if tok[0] != 1:
         raise ValueError("packed sequences: token arrays must have a leading dimension of 1")
-    if cu_seqlens.numel() < 1:
+    n = cu_seqlens.numel()
+    if n < 1:
         raise ValueError("cu_seqlens: at least one offset is needed")
-    _check(cu_seqlens, "cu_seqlens", (cu_seqlens.numel(),), torch.int32)
-    same_device(cu_seqlens, "cu_seqlens", device)
-    a.batch, a.seqlen = cu_seqlens.numel() - 1, L
-    a.cu_seqlens = cu_seqlens.data_ptr()
-    a.max_seqlen = int(L if max_seqlen is None else max_seqlen)
-    return a.batch
+    expect(cu_seqlens, "cu_seqlens", (n,), torch.int32, dev)
+    return n - 1, cu_seqlens.data_ptr(), int(tok[1] if max_seqlen is None else max_seqlen)
 
 
-def _take_slots(a, slots, rows, pool, device):
-    _check(slots, "slots", (rows,), torch.int32)
-    same_device(slots, "slots", device)
-    if pool is None:
-        raise ValueError("slots need a pool: h, or h_out for records that start from zero")
-    a.slots, a.nslots = slots.data_ptr(), pool.shape[0]
-
-
-def _workspace(need, given, device):
+def workspace_of(need, given, dev):
+    """(tensor to keep, address, bytes): `given` where it is large enough."""
     if need == 0:
-        return None
+        return None, 0, 0
     if given is None or given.numel() * given.element_size() < need:
-        return torch.empty(int(need), dtype=torch.uint8, device=device)
-    _check(given, "workspace", given.shape, given.dtype)
-    same_device(given, "workspace", device)
-    return given
+        given = torch.empty(need, dtype=torch.uint8, device=dev)
+    else:
+        expect(given, "workspace", given.shape, given.dtype, dev)
+    return given, given.data_ptr(), given.numel() * given.element_size()
+
+
+def address(t: Optional[torch.Tensor]) -> int:
+    return 0 if t is None else t.data_ptr()
 
 
 def m3_delta_supported(dstate: int, headdim: int, io_dtype: int) -> bool:
@@ -155,31 +168,38 @@ def m3_delta_fwd(q, k, v, g, beta, h: Optional[torch.Tensor] = None, *, scale: O
     ``slots`` that is the default.  Without ``return_state`` and ``h_out`` no
     state is written."""
     lib = load_library()
-    Bx, L, H, G, N, P = _shapes(q, k, v, g, beta, False)
-    a = DeltaArgs()
-    _common(a, H, G, N, P, _io_code(q.dtype), scale, l2norm, norm_eps)
-    rows = _rows(a, cu_seqlens, max_seqlen, Bx, L, q.device)
-    with on_device_of(q, stream) as handle:
+    tok, H, G, N, P, io, dev = _shapes(q, k, v, g, beta, False)
+    rows, cu, longest = _rows(cu_seqlens, max_seqlen, tok, dev)
+    handle, ctx = enter(dev, stream)
+    try:
+        nslots = at = 0
         if slots is not None:
-            _take_slots(a, slots, rows, h if h is not None else h_out, q.device)
+            expect(slots, "slots", (rows,), torch.int32, dev)
+            pool = h if h is not None else h_out
+            if pool is None:
+                raise ValueError("slots need a pool: h, or h_out for records that start from zero")
+            nslots, at = pool.shape[0], slots.data_ptr()
             if h_out is None and return_state:
                 h_out = h
         elif h_out is None and return_state:
-            h_out = torch.empty(rows, H, N, P, dtype=torch.float32, device=q.device)
-        for t, name in ((h, "h"), (h_out, "h_out")):
-            if t is not None:
-                _check(t, name, (a.nslots if slots is not None else rows, H, N, P), torch.float32)
-                same_device(t, name, q.device)
+            h_out = torch.empty((rows, H, N, P), dtype=torch.float32, device=dev)
+        record = (nslots if slots is not None else rows, H, N, P)
+        if h is not None:
+            expect(h, "h", record, torch.float32, dev)
+        if h_out is not None:
+            expect(h_out, "h_out", record, torch.float32, dev)
         if o is None:
             o = torch.empty_like(v)
-        _check(o, "o", v.shape, v.dtype)
-        same_device(o, "o", q.device)
-        a.q, a.k, a.v, a.g, a.beta = (t.data_ptr() for t in (q, k, v, g, beta))
-        a.h_in, a.o, a.h_out = _ptr(h), o.data_ptr(), _ptr(h_out)
-        ws = _workspace(lib.m3_delta_workspace_bytes(ctypes.byref(a)), workspace, q.device)
-        if ws is not None:
-            a.workspace, a.workspace_bytes = ws.data_ptr(), ws.numel() * ws.element_size()
-        st = lib.m3_delta_fwd(ctypes.byref(a), handle)
+        else:
+            expect(o, "o", v.shape, v.dtype, dev)
+        sizes = (rows, tok[1], H, G, P, N, io, 1 if l2norm else 0, N ** -0.5 if scale is None else scale, norm_eps)
+        need = lib.m3_delta_workspace_bytes(_pack_fwd(*sizes, 0, 0, 0, 0, 0, 0, 0, 0, cu, longest, 0, 0, 0, 0))
+        ws, wp, wn = workspace_of(need, workspace, dev)
+        st = lib.m3_delta_fwd(_pack_fwd(*sizes, q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(), beta.data_ptr(),
+                                        address(h), o.data_ptr(), address(h_out), cu, longest, at, nslots, wp, wn), handle)
+    finally:
+        if ctx is not None:
+            ctx.close()
     if st != 0:
         raise M3Error(st, "m3_delta_fwd")
     return o, h_out
@@ -187,11 +207,10 @@ def m3_delta_fwd(q, k, v, g, beta, h: Optional[torch.Tensor] = None, *, scale: O
 
 def m3_delta_workspace_bytes(q, v, *, cu_seqlens=None, max_seqlen=None) -> int:
     """Workspace bytes of m3_delta_fwd on token arrays like q and v."""
-    Bx, L, G, N = q.shape
-    a = DeltaArgs()
-    _common(a, v.shape[2], G, N, v.shape[3], _io_code(q.dtype), None, False, 0.0)
-    _rows(a, cu_seqlens, max_seqlen, Bx, L, q.device)
-    return int(load_library().m3_delta_workspace_bytes(ctypes.byref(a)))
+    tok, (G, N), (H, P) = tuple(q.shape[:2]), q.shape[2:], v.shape[2:]
+    rows, cu, longest = _rows(cu_seqlens, max_seqlen, tok, q.device)
+    return load_library().m3_delta_workspace_bytes(
+        _pack_fwd(rows, tok[1], H, G, P, N, _io_code(q.dtype), 0, 1.0, 0.0, 0, 0, 0, 0, 0, 0, 0, 0, cu, longest, 0, 0, 0, 0))
 
 
 def m3_delta_step(q, k, v, g, beta, h: torch.Tensor, *, scale: Optional[float] = None,
@@ -199,21 +218,24 @@ def m3_delta_step(q, k, v, g, beta, h: torch.Tensor, *, scale: Optional[float] =
                   slots: Optional[torch.Tensor] = None, stream=None):
     """One token for every row: q, k [Bt, G, N], v [Bt, H, P], g, beta [Bt, H];
     ``h`` is updated in place.  Returns o_t."""
-    Bt, _, H, G, N, P = _shapes(q, k, v, g, beta, True)
-    a = DeltaStepArgs(batch=Bt)
-    _common(a, H, G, N, P, _io_code(q.dtype), scale, l2norm, norm_eps)
+    (Bt,), H, G, N, P, io, dev = _shapes(q, k, v, g, beta, True)
+    nslots = at = 0
     if slots is not None:
-        _take_slots(a, slots, Bt, h, q.device)
-    _check(h, "h", (h.shape[0] if slots is not None else Bt, H, N, P), torch.float32)
-    same_device(h, "h", q.device)
-    with on_device_of(q, stream) as handle:
+        expect(slots, "slots", (Bt,), torch.int32, dev)
+        nslots, at = h.shape[0], slots.data_ptr()
+    expect(h, "h", (nslots if slots is not None else Bt, H, N, P), torch.float32, dev)
+    handle, ctx = enter(dev, stream)
+    try:
         if o is None:
             o = torch.empty_like(v)
-        _check(o, "o", v.shape, v.dtype)
-        same_device(o, "o", q.device)
-        a.q, a.k, a.v, a.g, a.beta = (t.data_ptr() for t in (q, k, v, g, beta))
-        a.h, a.o = h.data_ptr(), o.data_ptr()
-        st = load_library().m3_delta_step(ctypes.byref(a), handle)
+        else:
+            expect(o, "o", v.shape, v.dtype, dev)
+        st = load_library().m3_delta_step(
+            _pack_step(Bt, H, G, P, N, io, 1 if l2norm else 0, N ** -0.5 if scale is None else scale, norm_eps, q.data_ptr(),
+                       k.data_ptr(), v.data_ptr(), g.data_ptr(), beta.data_ptr(), h.data_ptr(), o.data_ptr(), at, nslots), handle)
+    finally:
+        if ctx is not None:
+            ctx.close()
     if st != 0:
         raise M3Error(st, "m3_delta_step")
     return o
@@ -228,30 +250,30 @@ def m3_delta_bwd(q, k, v, g, beta, do, h: Optional[torch.Tensor] = None,
     to every input as given; ``state_grad`` also returns that of the input
     state (a zero state when ``h`` is None)."""
     lib = load_library()
-    Bx, L, H, G, N, P = _shapes(q, k, v, g, beta, False)
-    b = DeltaBwdArgs()
-    a = b.in_
-    _common(a, H, G, N, P, _io_code(q.dtype), scale, l2norm, norm_eps)
-    rows = _rows(a, cu_seqlens, max_seqlen, Bx, L, q.device)
-    _check(do, "do", v.shape, v.dtype)
-    same_device(do, "do", q.device)
+    tok, H, G, N, P, io, dev = _shapes(q, k, v, g, beta, False)
+    rows, cu, longest = _rows(cu_seqlens, max_seqlen, tok, dev)
+    expect(do, "do", v.shape, v.dtype, dev)
     for t, name in ((h, "h"), (dh_out, "dh_out")):
         if t is not None:
-            _check(t, name, (rows, H, N, P), torch.float32)
-            same_device(t, name, q.device)
-    with on_device_of(q, stream) as handle:
-        f32 = dict(dtype=torch.float32, device=q.device)
+            expect(t, name, (rows, H, N, P), torch.float32, dev)
+    handle, ctx = enter(dev, stream)
+    try:
+        f32 = dict(dtype=torch.float32, device=dev)
         r = DeltaGrads(torch.empty(q.shape, **f32), torch.empty(k.shape, **f32),
                        torch.empty(v.shape, **f32), torch.empty(g.shape, **f32),
                        torch.empty(beta.shape, **f32),
-                       torch.empty(rows, H, N, P, **f32) if state_grad else None)
-        a.q, a.k, a.v, a.g, a.beta, a.h_in = (_ptr(t) for t in (q, k, v, g, beta, h))
-        b.dout, b.dh_out = do.data_ptr(), _ptr(dh_out)
-        b.dq, b.dk, b.dv, b.dg, b.dbeta, b.dh_in = (_ptr(t) for t in r)
-        ws = _workspace(lib.m3_delta_bwd_workspace_bytes(ctypes.byref(b)), workspace, q.device)
-        if ws is not None:
-            a.workspace, a.workspace_bytes = ws.data_ptr(), ws.numel() * ws.element_size()
-        st = lib.m3_delta_bwd(ctypes.byref(b), handle)
+                       torch.empty((rows, H, N, P), **f32) if state_grad else None)
+
+        def args(wp, wn):
+            return _pack_bwd(rows, tok[1], H, G, P, N, io, 1 if l2norm else 0, N ** -0.5 if scale is None else scale, norm_eps,
+                             q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(), beta.data_ptr(), address(h), 0, 0, cu,
+                             longest, 0, 0, wp, wn, do.data_ptr(), address(dh_out), *(address(t) for t in r))
+
+        ws, wp, wn = workspace_of(lib.m3_delta_bwd_workspace_bytes(args(0, 0)), workspace, dev)
+        st = lib.m3_delta_bwd(args(wp, wn), handle)
+    finally:
+        if ctx is not None:
+            ctx.close()
     if st != 0:
         raise M3Error(st, "m3_delta_bwd")
     return r

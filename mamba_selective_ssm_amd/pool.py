@@ -10,12 +10,13 @@ device; no call waits for it.
 from __future__ import annotations
 
 import ctypes
+import math
 from typing import Optional, Sequence
 
 import torch
 
-from .binding import M3Error, _check, _ptr, load_library
-from .delta import on_device_of
+from .binding import M3Error, load_library
+from .delta import address, enter, expect, packer, workspace_of
 
 MAX_ARRAYS = 8
 _vp, _i64, _i32 = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32
@@ -42,54 +43,27 @@ class PoolCompactArgs(ctypes.Structure):
                 ("count", _vp), ("workspace", _vp), ("workspace_bytes", ctypes.c_size_t)]
 
 
-def _desc(pool: Sequence[torch.Tensor], name: str) -> PoolDesc:
+_pack_copy, _pack_fork, _pack_compact = packer(PoolCopyArgs), packer(PoolForkArgs), packer(PoolCompactArgs)
+
+
+def _desc(pool: Sequence[torch.Tensor], name: str):
+    """(slots, device, the values of an m3_pool)."""
     arrays = (pool,) if isinstance(pool, torch.Tensor) else tuple(pool)
-    if not 1 <= len(arrays) <= MAX_ARRAYS:
-        raise ValueError("%s: 1 to %d arrays, got %d" % (name, MAX_ARRAYS, len(arrays)))
-    d = PoolDesc(narrays=len(arrays))
+    n = len(arrays)
+    if not 1 <= n <= MAX_ARRAYS:
+        raise ValueError("%s: 1 to %d arrays, got %d" % (name, MAX_ARRAYS, n))
+    dev, slots = arrays[0].device, None
+    at, rows = [0] * MAX_ARRAYS, [0] * MAX_ARRAYS
+    if dev.type != "cuda":
+        raise ValueError("%s[0] must be a device tensor" % name)
     for i, t in enumerate(arrays):
-        if t.dim() < 1:
+        shape = tuple(t.shape)
+        if not shape:
             raise ValueError("%s[%d] has no slot axis" % (name, i))
-        _check(t, "%s[%d]" % (name, i), (arrays[0].shape[0],) + tuple(t.shape[1:]), t.dtype)
-        if t.device != arrays[0].device:
-            raise ValueError("%s[%d] is on %s, the first array on %s" % (name, i, t.device, arrays[0].device))
-        d.data[i] = t.data_ptr()
-        row = t.element_size()
-        for n in t.shape[1:]:
-            row *= n
-        d.row_bytes[i] = row
-    d.slots = arrays[0].shape[0]
-    return d
-
-
-def _first(pool):
-    return pool if isinstance(pool, torch.Tensor) else pool[0]
-
-
-def _index(t, name, n, device):
-    _check(t, name, (n,), torch.int32)
-    if t.device != device:
-        raise ValueError("%s is on %s, the pool on %s" % (name, t.device, device))
-
-
-def _bytes(need, given, device):
-    if need == 0:
-        return None
-    if given is None or given.numel() * given.element_size() < need:
-        return torch.empty(int(need), dtype=torch.uint8, device=device)
-    _check(given, "workspace", given.shape, given.dtype)
-    if given.device != device:
-        raise ValueError("workspace is on %s, the pool on %s" % (given.device, device))
-    return given
-
-
-def _run(fn, a, need, workspace, device, handle, what):
-    ws = _bytes(need, workspace, device)
-    if ws is not None:
-        a.workspace, a.workspace_bytes = ws.data_ptr(), ws.numel() * ws.element_size()
-    st = fn(ctypes.byref(a), handle)
-    if st != 0:
-        raise M3Error(st, what)
+        slots = shape[0] if slots is None else slots
+        expect(t, "%s[%d]" % (name, i), (slots,) + shape[1:], t.dtype, dev)
+        at[i], rows[i] = t.data_ptr(), t.element_size() * math.prod(shape[1:])
+    return slots, dev, (slots, n, 0, *at, *rows)
 
 
 def m3_pool_copy(src, dst, src_slot: torch.Tensor, dst_slot: torch.Tensor, *,
@@ -98,16 +72,23 @@ def m3_pool_copy(src, dst, src_slot: torch.Tensor, dst_slot: torch.Tensor, *,
     ``src``), as if every source were read first; the last pair that names a
     slot wins; src_slot[i] < 0 clears the slot; pairs outside are left out."""
     lib = load_library()
-    a = PoolCopyArgs(src=_desc(src, "src"), dst=_desc(dst, "dst"), count=src_slot.numel())
-    dev = _first(dst).device
-    if _first(src).device != dev:
-        raise ValueError("src is on %s, dst on %s" % (_first(src).device, dev))
-    _index(src_slot, "src_slot", a.count, dev)
-    _index(dst_slot, "dst_slot", a.count, dev)
-    a.src_slot, a.dst_slot = src_slot.data_ptr(), dst_slot.data_ptr()
-    with on_device_of(_first(dst), stream) as handle:
-        need = lib.m3_pool_copy_workspace_bytes(ctypes.byref(a))
-        _run(lib.m3_pool_copy, a, need, workspace, dev, handle, "m3_pool_copy")
+    _, dev, s = _desc(src, "src")
+    _, dd, d = _desc(dst, "dst")
+    if dd != dev:
+        raise ValueError("src is on %s, dst on %s" % (dev, dd))
+    n = src_slot.numel()
+    expect(src_slot, "src_slot", (n,), torch.int32, dev)
+    expect(dst_slot, "dst_slot", (n,), torch.int32, dev)
+    handle, ctx = enter(dev, stream)
+    try:
+        head = (*s, *d, src_slot.data_ptr(), dst_slot.data_ptr(), n)
+        ws, wp, wn = workspace_of(lib.m3_pool_copy_workspace_bytes(_pack_copy(*head, 0, 0)), workspace, dev)
+        st = lib.m3_pool_copy(_pack_copy(*head, wp, wn), handle)
+    finally:
+        if ctx is not None:
+            ctx.close()
+    if st != 0:
+        raise M3Error(st, "m3_pool_copy")
 
 
 def m3_pool_fork(pool, live: torch.Tensor, parents: torch.Tensor, *,
@@ -116,19 +97,26 @@ def m3_pool_fork(pool, live: torch.Tensor, parents: torch.Tensor, *,
     """For each parents[i] the lowest free slot, a copy of that record (< 0: a
     cleared one) in it, marked in ``live_out`` (default: ``live`` itself).
     Returns the slots, -1 where none was left or the parent is not live."""
-    lib = load_library()
-    dev = _first(pool).device
-    a = PoolForkArgs(pool=_desc(pool, "pool"), count=parents.numel())
-    _index(live, "live", a.pool.slots, dev)
-    _index(parents, "parents", a.count, dev)
+    slots, dev, d = _desc(pool, "pool")
+    n = parents.numel()
     live_out = live if live_out is None else live_out
-    _index(live_out, "live_out", a.pool.slots, dev)
-    with on_device_of(_first(pool), stream) as handle:
+    expect(live, "live", (slots,), torch.int32, dev)
+    expect(live_out, "live_out", (slots,), torch.int32, dev)
+    expect(parents, "parents", (n,), torch.int32, dev)
+    handle, ctx = enter(dev, stream)
+    try:
         if children is None:
             children = torch.empty_like(parents)
-        _index(children, "children", a.count, dev)
-        a.live, a.live_out, a.parents, a.children = (t.data_ptr() for t in (live, live_out, parents, children))
-        _run(lib.m3_pool_fork, a, 4 * a.count, workspace, dev, handle, "m3_pool_fork")
+        else:
+            expect(children, "children", (n,), torch.int32, dev)
+        ws, wp, wn = workspace_of(4 * n, workspace, dev)
+        st = load_library().m3_pool_fork(_pack_fork(*d, live.data_ptr(), live_out.data_ptr(), parents.data_ptr(),
+                                                    children.data_ptr(), n, wp, wn), handle)
+    finally:
+        if ctx is not None:
+            ctx.close()
+    if st != 0:
+        raise M3Error(st, "m3_pool_fork")
     return children
 
 
@@ -139,28 +127,37 @@ def m3_pool_compact(pool, live: torch.Tensor, *, new_slot: Optional[torch.Tensor
     Returns new_slot: where each slot's record is now (-1: free).  ``count``
     (int32 [1]) receives the number of live records; ``live_out`` (may be
     ``live``) the new marks."""
-    lib = load_library()
-    dev = _first(pool).device
-    a = PoolCompactArgs(pool=_desc(pool, "pool"))
-    _index(live, "live", a.pool.slots, dev)
-    with on_device_of(_first(pool), stream) as handle:
+    slots, dev, d = _desc(pool, "pool")
+    expect(live, "live", (slots,), torch.int32, dev)
+    handle, ctx = enter(dev, stream)
+    try:
         if new_slot is None:
             new_slot = torch.empty_like(live)
-        for t, name, n in ((new_slot, "new_slot", a.pool.slots), (count, "count", 1),
-                           (live_out, "live_out", a.pool.slots)):
+        for t, name, n in ((new_slot, "new_slot", slots), (count, "count", 1), (live_out, "live_out", slots)):
             if t is not None:
-                _index(t, name, n, dev)
-        a.live, a.new_slot = live.data_ptr(), new_slot.data_ptr()
-        a.live_out, a.count = _ptr(live_out), _ptr(count)
-        _run(lib.m3_pool_compact, a, 4 * (a.pool.slots + 1), workspace, dev, handle, "m3_pool_compact")
+                expect(t, name, (n,), torch.int32, dev)
+        ws, wp, wn = workspace_of(4 * (slots + 1), workspace, dev)
+        st = load_library().m3_pool_compact(_pack_compact(*d, live.data_ptr(), address(live_out), new_slot.data_ptr(),
+                                                          address(count), wp, wn), handle)
+    finally:
+        if ctx is not None:
+            ctx.close()
+    if st != 0:
+        raise M3Error(st, "m3_pool_compact")
     return new_slot
 
 
 def m3_pool_free(live: torch.Tensor, slots: torch.Tensor, *, stream=None) -> None:
     """Marks the slots as free; entries outside the pool are left out."""
-    _index(live, "live", live.numel(), live.device)
-    _index(slots, "slots", slots.numel(), live.device)
-    with on_device_of(live, stream) as handle:
+    if live.device.type != "cuda":
+        raise ValueError("live must be a device tensor")
+    expect(live, "live", (live.numel(),), torch.int32, live.device)
+    expect(slots, "slots", (slots.numel(),), torch.int32, live.device)
+    handle, ctx = enter(live.device, stream)
+    try:
         st = load_library().m3_pool_free(live.data_ptr(), live.numel(), slots.data_ptr(), slots.numel(), handle)
+    finally:
+        if ctx is not None:
+            ctx.close()
     if st != 0:
         raise M3Error(st, "m3_pool_free")

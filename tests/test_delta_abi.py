@@ -246,5 +246,5 @@ def test_binding_refusals():
         m3_pool_copy((q,), (q,), torch.zeros(1, dtype=torch.int32), torch.zeros(1, dtype=torch.int32))
     with pytest.raises(ValueError):
         m3_pool_copy((), (), torch.zeros(1, dtype=torch.int32), torch.zeros(1, dtype=torch.int32))
-    with pytest.raises(TypeError):
-        m3_pool_free(torch.zeros(4), torch.zeros(1, dtype=torch.int32))
+    with pytest.raises(ValueError):
+        m3_pool_free(torch.zeros(4, dtype=torch.int32), torch.zeros(1, dtype=torch.int32))
