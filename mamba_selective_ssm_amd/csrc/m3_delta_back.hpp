@@ -137,17 +137,16 @@ __global__ __launch_bounds__(256) void delta_pre_kernel(const DeltaBwdParams bp)
 // T^T for T and dR for d U; E1 and E2 stand in the places of dR and dS and are
 // read one chunk ahead.
 template <typename IO, int N>
-__global__ __launch_bounds__(320) void delta_back_kernel(const DeltaBwdParams bp)
+__device__ __forceinline__ void delta_back(const DeltaBwdParams& bp, int64_t bid, char* wlds)
 {
-    using Cf = WalkCfg<IO, N, 1>;
+    using Cf = WalkCfg<IO, N, true>;
     constexpr int KP = Cf::KP, WP = Cf::WP, KB = Cf::KB, NT = Cf::NT, TI = Cf::TI, NBUF = Cf::NBUF;
     const DeltaParams& p = bp.f;
-    extern __shared__ __attribute__((aligned(16))) char wlds[];
     const int tid = threadIdx.x, lane = tid & 63, l = lane & 15, g = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), w = wave & 3;
     const int nsl = p.P / 16;
-    const int64_t idx = blockIdx.x >> 3;
-    const int64_t unit = (idx / nsl) * 8 + (blockIdx.x & 7);
+    const int64_t idx = bid >> 3;
+    const int64_t unit = (idx / nsl) * 8 + (bid & 7);
     if (unit >= (int64_t)p.rows * p.H) return;
     int64_t b64, h64;
     split_bh(unit, p.H, b64, h64);
@@ -157,7 +156,7 @@ __global__ __launch_bounds__(320) void delta_back_kernel(const DeltaBwdParams bp
     const int64_t ci0 = row.slot0 * p.H + h;
     const int nlast = (int)(row.len - (int64_t)(nch - 1) * kDC);
     if (wave == 4) {
-        walk_loader<IO, N, 1, true>(p, wlds, bp.ttf, row, h, p0, nch, nlast, lane);
+        walk_loader<IO, N, true, true>(p, wlds, bp.ttf, row, h, p0, nch, nlast, lane);
         return;
     }
     char* ex = wlds + Cf::ex + 16 * lane;
@@ -314,6 +313,18 @@ __global__ __launch_bounds__(320) void delta_back_kernel(const DeltaBwdParams bp
 #pragma unroll
                 for (int r = 0; r < 4; ++r) ho[(tr0 + 64 * i + r) * P] = S[i][r];
     }
+}
+
+// Both walks of the gradient: neither needs the other, and each alone waits
+// for its own chain most of the time.  All workgroups of one, then of the
+// other, so that a CU gets one of each.
+template <typename IO, int N>
+__global__ __launch_bounds__(320) void delta_walks_kernel(const DeltaBwdParams bp)
+{
+    extern __shared__ __attribute__((aligned(16))) char wlds[];
+    const unsigned n = gridDim.x / 2;   // a multiple of 8: the XCDs of both halves agree
+    if (blockIdx.x < n) delta_back<IO, N>(bp, blockIdx.x, wlds);
+    else delta_walk<IO, N, true>(bp.f, bp.S, bp.U, blockIdx.x - n, wlds);
 }
 
 // Sum over the four lane groups (g).
@@ -757,19 +768,20 @@ hipError_t bwd_n(const DeltaBwdParams& bp, hipStream_t stream)
     const DeltaParams& p = bp.f;
     hipError_t e = launch_delta_chunks<IO, N, true>(p, bp.ttf, bp.atf, stream);
     if (e != hipSuccess) return e;
-    if ((e = launch_delta_walk<IO, N, 1, true>(p, bp.S, bp.U, stream)) != hipSuccess) return e;
     const int64_t blocks = (int64_t)p.rows * p.nc * p.H;
     if (blocks > 0) {
         hipLaunchKernelGGL((delta_pre_kernel<IO, N>), dim3((unsigned)blocks), dim3(256), 0, stream, bp);
         if ((e = hipGetLastError()) != hipSuccess) return e;
     }
     if (p.rows > 0) {
-        auto* const back = &delta_back_kernel<IO, N>;
-        constexpr size_t lds = WalkCfg<IO, N, 1>::total;
-        static const hipError_t attr = delta_allow_lds(back, lds);
+        using Cf = WalkCfg<IO, N, true>;
+        auto* const walks = &delta_walks_kernel<IO, N>;
+        static_assert(Cf::total <= 160 * 1024, "a workgroup's LDS");
+        static const hipError_t attr = delta_allow_lds(walks, Cf::total);
         if (attr != hipSuccess) return attr;
-        const int64_t walks = ((int64_t)p.rows * p.H + 7) / 8 * 8 * (p.P / 16);
-        hipLaunchKernelGGL(back, dim3((unsigned)walks), dim3(320), lds, stream, bp);
+        const int64_t n = ((int64_t)p.rows * p.H + 7) / 8 * 8 * (p.P / 16);
+        const size_t lds = Cf::total;
+        hipLaunchKernelGGL(walks, dim3((unsigned)(2 * n)), dim3(64 * Cf::waves), lds, stream, bp);
         if ((e = hipGetLastError()) != hipSuccess) return e;
     }
     switch (p.P) {

@@ -11,7 +11,7 @@ hipError_t fwd_n(const DeltaParams& p, hipStream_t stream)
 {
     const hipError_t e = launch_delta_chunks<IO, N, false>(p, nullptr, nullptr, stream);
     if (e != hipSuccess) return e;
-    return launch_delta_walk<IO, N, 1, false>(p, nullptr, nullptr, stream);
+    return launch_delta_walk<IO, N>(p, stream);
 }
 
 template <typename IO>

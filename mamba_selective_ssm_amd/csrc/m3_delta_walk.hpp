@@ -7,39 +7,41 @@
 
 namespace m3 {
 
-// The walk over one row's chunks for one head and 16 NS columns of V.
+// The walk over one row's chunks for one head and 16 columns of V.
 //
 // Per chunk:  R = beta V - sp (K S) | U = T R | S <- e^G_last S + K^T (d U),
 // and O = so (Q S) + A U with the chunk's first S.  Each product needs the one
 // before it, so the walk's time is this chain's, chunk after chunk, and all
 // that is not on it is kept out of it:
-//   - four state wavefronts per 16 columns run the chain, wave w on row tile w
+//   - four state wavefronts run the chain, wave w on row tile w
 //     of each product; a result leaves as planes in operand order (tile_row),
 //     so that all four read it back with plain 16-byte reads after a barrier;
 //   - a loader wavefront moves K, T, V and the factors from memory straight to
-//     LDS, NBUF - 1 chunks ahead; they are first operands, the same for all
-//     columns;
-//   - two output wavefronts per 16 columns make O from the S and U planes, Q S
+//     LDS, NBUF - 1 chunks ahead;
+//   - two output wavefronts make O from the S and U planes, Q S
 //     while the state goes through T, A U during the next chunk's first stage.
 //
 // K rows lie in LDS in blocks of 8 values whose place is permuted by the row
 // (k_block), which keeps both the row-wise and the transposed reads free of
 // bank conflicts without padding, as the direct loads need it.
-template <typename IO, int N, int NS> struct WalkCfg {
+// TRAIN (the gradient's two walks, which run beside each other): no output
+// wavefronts, and buffers for one chunk ahead only, so that two workgroups fit
+// on a CU.
+template <typename IO, int N, bool TRAIN> struct WalkCfg {
     static constexpr int KP = DeltaPlanes<IO>::io, WP = DeltaPlanes<IO>::wide, OP = DeltaPlanes<IO>::out;
     static constexpr bool DIRECT = KP == 1;           // io values are operands as they are: loads go straight to LDS
-    static constexpr int NBUF = DIRECT ? 3 : 2;
+    static constexpr int NBUF = DIRECT && !TRAIN ? 3 : 2;
     static constexpr int KB = N / 32, NT = N / 16, TI = (NT + 3) / 4;
-    static constexpr int waves = 6 * NS + 1;
-    // bytes of one buffer (T apart: float32 calls have room for one T only)
-    static constexpr int k = 0, f = k + KP * 64 * N * 2, v = f + 5 * 256, buf = v + (DIRECT ? 64 * NS * 32 : 0);
-    static constexpr int tsize = kTriBlocks * WP * 1024, TB = DIRECT ? NBUF : 1;
+    static constexpr int outs = TRAIN ? 0 : 2, waves = 4 + outs + 1;
+    // bytes of one buffer (T apart: those with one chunk ahead have one T)
+    static constexpr int k = 0, f = k + KP * 64 * N * 2, v = f + 5 * 256, buf = v + (DIRECT ? 64 * 32 : 0);
+    static constexpr int tsize = kTriBlocks * WP * 1024, TB = DIRECT && !TRAIN ? NBUF : 1;
     static constexpr int t = NBUF * buf;
-    // then per column group the planes of S, R, d U, U, and the rows of O
+    // then the planes of S, R, d U, U, and the rows of O
     static constexpr int ex = t + TB * tsize, s = 0, r = s + WP * KB * 1024, u2 = r + WP * 2048, u = u2 + WP * 2048,
-                         o = u + OP * 2048, ex1 = o + 64 * 16 * (int)sizeof(IO), total = ex + NS * ex1;
+                         o = u + OP * 2048, total = ex + (TRAIN ? u : o + 64 * 16 * (int)sizeof(IO));
     // loads of one chunk by the loader (DIRECT): T, factors, K, V
-    static constexpr int loads = kTriBlocks * WP + 2 + 64 * N * 2 / 1024 + 2 * NS;
+    static constexpr int loads = kTriBlocks * WP + 2 + 64 * N * 2 / 1024 + 2;
 };
 
 // Where block j (8 values) of row t lies in its row.
@@ -71,12 +73,13 @@ template <int n> __device__ __forceinline__ void wait_loads()
 // The loader wavefront of a walk: K, the triangle `tri`, the factors and (not
 // REV) V of each chunk to LDS, NBUF - 1 steps ahead of their use.  REV: chunks
 // from the last to the first.
-template <typename IO, int N, int NS, bool REV>
+template <typename IO, int N, bool TRAIN, bool REV>
 __device__ __forceinline__ void walk_loader(const DeltaParams& p, char* wlds, const bf16* tri, const DeltaRow& row, int h,
                                             int p0, int nch, int nlast, int lane)
 {
-    using Cf = WalkCfg<IO, N, NS>;
+    using Cf = WalkCfg<IO, N, TRAIN>;
     constexpr int KP = Cf::KP, WP = Cf::WP, NBUF = Cf::NBUF;
+    constexpr bool T1 = Cf::TB == 1;
     const int rs = p.G * N, vs = p.H * p.P;
     const int64_t ci0 = row.slot0 * p.H + h;
     const IO* kp = reinterpret_cast<const IO*>(p.k) + (row.start * p.G + h / (p.H / p.G)) * N;
@@ -90,28 +93,32 @@ __device__ __forceinline__ void walk_loader(const DeltaParams& p, char* wlds, co
         for (int i = 0; i < kTriBlocks * WP; ++i)
             if (i >= i0 && i < i1) to_lds16(dst + 1024 * i, src + 1024 * i + 16 * lane);
     };
-    auto stage = [&](int s) {
+    // factors, V, K: loads i0..i1-1 of `head`
+    constexpr int nk = 64 * N * 2 / 1024, nv = REV ? 0 : 2, head = 2 + nv + nk;
+    auto stage = [&](int s, int i0, int i1) {
         const int c = REV ? nch - 1 - s : s;
         char* buf = wlds + (s % NBUF) * Cf::buf;
         const int end = c == nch - 1 ? nlast - 1 : kDC - 1;   // last row to read
         const IO* kc = kp + (int64_t)c * kDC * rs;
         constexpr int RPL = 512 / N;   // K rows of one load
         const float* fsrc = p.sc + (ci0 + (int64_t)c * p.H) * (kDScal * 64);
-        to_lds16(buf + Cf::f, fsrc + 4 * lane);
-        to_lds4(buf + Cf::f + 1024, fsrc + 256 + lane);
+        if (i0 == 0) {
+            to_lds16(buf + Cf::f, fsrc + 4 * lane);
+            to_lds4(buf + Cf::f + 1024, fsrc + 256 + lane);
+        }
         if constexpr (Cf::DIRECT) {
 #pragma unroll
-            for (int i = 0; i < 64 / RPL; ++i) {
+            for (int i = 0; i < nk; ++i) {
+                if (2 + nv + i < i0 || 2 + nv + i >= i1) continue;
                 const int t = RPL * i + lane / (N / 8), j = k_block<N>(t, lane % (N / 8));
                 to_lds16(buf + Cf::k + 1024 * i, kc + (t < end ? t : end) * rs + 8 * j);
             }
-            if constexpr (!REV) {
+            if (!REV && i0 == 0) {
                 const IO* vc = vp + (int64_t)c * kDC * vs;
-                constexpr int VPL = 32 / NS;   // V rows of one load
 #pragma unroll
-                for (int i = 0; i < 2 * NS; ++i) {
-                    const int t = VPL * i + lane / (2 * NS);
-                    to_lds16(buf + Cf::v + 1024 * i, vc + (t < end ? t : end) * vs + 8 * (lane % (2 * NS)));
+                for (int i = 0; i < 2; ++i) {
+                    const int t = 32 * i + lane / 2;
+                    to_lds16(buf + Cf::v + 1024 * i, vc + (t < end ? t : end) * vs + 8 * (lane % 2));
                 }
             }
         } else {
@@ -137,7 +144,7 @@ __device__ __forceinline__ void walk_loader(const DeltaParams& p, char* wlds, co
 #pragma unroll
     for (int s = 0; s < NBUF - 1; ++s)
         if (s < nch) {
-            stage(s);
+            stage(s, 0, head);
             if (s < Cf::TB) stage_t(s, 0, 3 * kTriBlocks);
         }
     asm volatile("" ::: "memory");
@@ -146,43 +153,47 @@ __device__ __forceinline__ void walk_loader(const DeltaParams& p, char* wlds, co
     for (int s = 0; s < nch; ++s) {
         // a third of the loads beside each stage: a load takes some 30 cycles
         // to issue, all of one chunk longer than a stage
+        constexpr int third = (head + 18) / 3;
+        constexpr int k1 = Cf::DIRECT && !T1 && third < head ? third : head, t1 = 2 * third > head ? 2 * third - head : 0;
         const bool more = s + NBUF - 1 < nch;
-        if (more) stage(s + NBUF - 1);
+        if (more) stage(s + NBUF - 1, 0, k1);
         barrier();   // R
-        if (Cf::DIRECT && more) stage_t(s + NBUF - 1, 0, 9);
+        if (!T1 && more) {
+            if (k1 < head) stage(s + NBUF - 1, k1, head);
+            stage_t(s + NBUF - 1, 0, t1);
+        }
         barrier();   // U: a single T is free
-        if (Cf::DIRECT) {
-            if (more) stage_t(s + NBUF - 1, 9, 18);
+        if (!T1) {
+            if (more) stage_t(s + NBUF - 1, t1, 18);
         } else if (s + 1 < nch) {
             stage_t(s + 1, 0, 18);
         }
         asm volatile("" ::: "memory");
         // the next chunk has landed
-        constexpr int loads = Cf::loads - (REV ? 2 * NS : 0);
-        if (Cf::DIRECT && NBUF == 3 && more) wait_loads<loads>();
+        constexpr int loads = Cf::loads - (REV ? 2 : 0);
+        if (NBUF == 3 && more) wait_loads<loads>();
         else __builtin_amdgcn_s_waitcnt(0);
         barrier();   // S
     }
 }
 
-template <typename IO, int N, int NS, bool TRAIN>
-__global__ __launch_bounds__(64 * (6 * NS + 1)) void delta_walk_kernel(const DeltaParams p, float* Sbuf, float* Ubuf)
+template <typename IO, int N, bool TRAIN>
+__device__ __forceinline__ void delta_walk(const DeltaParams& p, float* Sbuf, float* Ubuf, int64_t bid, char* wlds)
 {
-    using Cf = WalkCfg<IO, N, NS>;
+    using Cf = WalkCfg<IO, N, TRAIN>;
     constexpr int KP = Cf::KP, WP = Cf::WP, OP = Cf::OP, KB = Cf::KB, NT = Cf::NT, TI = Cf::TI, NBUF = Cf::NBUF;
-    extern __shared__ __attribute__((aligned(16))) char wlds[];
 
     const int tid = threadIdx.x, lane = tid & 63, l = lane & 15, g = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     // the slices of one (row, head) run on one XCD and share its L2
-    const int nsl = p.P / (16 * NS);
-    const int64_t idx = blockIdx.x >> 3;
-    const int64_t unit = (idx / nsl) * 8 + (blockIdx.x & 7);
+    const int nsl = p.P / 16;
+    const int64_t idx = bid >> 3;
+    const int64_t unit = (idx / nsl) * 8 + (bid & 7);
     if (unit >= (int64_t)p.rows * p.H) return;
     int64_t b64, h64;
     split_bh(unit, p.H, b64, h64);
     const int b = (int)b64, h = (int)h64;
-    const int p0 = (int)(idx % nsl) * (16 * NS);   // first column of the workgroup
+    const int p0 = (int)(idx % nsl) * 16;   // first column
     const DeltaRow row = delta_row(p, b);
     const int64_t rec = TRAIN ? b : delta_record(p, b, tid, 64 * Cf::waves, reinterpret_cast<int*>(wlds));
     const int nch = (int)((row.len + kDC - 1) / kDC);
@@ -192,32 +203,23 @@ __global__ __launch_bounds__(64 * (6 * NS + 1)) void delta_walk_kernel(const Del
     // and T's rows there are the identity's, so they write and decay nothing.
     const int nlast = (int)(row.len - (int64_t)(nch - 1) * kDC);   // tokens of the last chunk
 
-    if (wave == 6 * NS) {
-        walk_loader<IO, N, NS, false>(p, wlds, p.tf, row, h, p0, nch, nlast, lane);
+    if (wave == Cf::waves - 1) {
+        walk_loader<IO, N, TRAIN, false>(p, wlds, p.tf, row, h, p0, nch, nlast, lane);
         return;
     }
 
     const f32x4 fz = {0.f, 0.f, 0.f, 0.f};
-    const int cg = wave < 4 * NS ? wave >> 2 : (wave - 4 * NS) >> 1;   // column group
-    char* ex = wlds + Cf::ex + cg * Cf::ex1 + 16 * lane;
+    char* ex = wlds + Cf::ex + 16 * lane;
 
-    if (wave >= 4 * NS) {   // output: row tiles 2 o, 2 o + 1
-        if (TRAIN) {
-            __syncthreads();
-            for (int c = 0; c < nch; ++c) {
-                __syncthreads();
-                __syncthreads();
-                __syncthreads();
-            }
-            return;
-        }
+    if constexpr (!TRAIN)
+    if (wave >= 4) {   // output: row tiles 2 o, 2 o + 1
         // No load depends on a branch: where one might, a wait for the chunk's
         // operands would also wait for those of the chunk after it.
         auto output = [&](auto half_) {
         constexpr int o = decltype(half_)::value;
         const IO* qp = reinterpret_cast<const IO*>(p.q) + (row.start * p.G + h / (p.H / p.G)) * N + 8 * g;
-        IO* op = reinterpret_cast<IO*>(p.o) + (row.start * p.H + h) * p.P + p0 + 16 * cg;
-        IO* so = reinterpret_cast<IO*>(wlds + Cf::ex + cg * Cf::ex1 + Cf::o) + 32 * o * 16;   // this wave's rows
+        IO* op = reinterpret_cast<IO*>(p.o) + (row.start * p.H + h) * p.P + p0;
+        IO* so = reinterpret_cast<IO*>(wlds + Cf::ex + Cf::o) + 32 * o * 16;   // this wave's rows
         RawRow8<IO> q[2][KB];
         struct Tri {
             bf16x8 a0[2][OP], a1[2][OP];
@@ -330,7 +332,7 @@ __global__ __launch_bounds__(64 * (6 * NS + 1)) void delta_walk_kernel(const Del
     const int tr0 = 32 * (w >> 1) + 4 * (w & 1) + 8 * g;   // first row of tile w in this lane
     const int nb = (w >> 1) + 1;                           // 32-token blocks that tile w of T spans
     const int half = 8 * (w & 1);                          // its place in an operand's 16 bytes
-    const int col = p0 + 16 * cg + l;
+    const int col = p0 + l;
     f32x4 S[TI];
     const float* hin = p.h_in != nullptr && rec >= 0 ? p.h_in + (rec * p.H + h) * (int64_t)(N * p.P) + col : nullptr;
 #pragma unroll
@@ -397,22 +399,22 @@ __global__ __launch_bounds__(64 * (6 * NS + 1)) void delta_walk_kernel(const Del
                     k8[kb][j] = *reinterpret_cast<const bf16x8*>(buf + Cf::k + j * (64 * N * 2) + t * (2 * N) +
                                                                  16 * k_block<N>(t, 4 * kb + g));
             }
-#pragma unroll
-            for (int kb = 0; kb < 2; ++kb)
-#pragma unroll
-                for (int j = 0; j < WP; ++j)
-                    t8[kb][j] = *reinterpret_cast<const bf16x8*>(tb + (low_block(w, kb < nb ? kb : 0) * WP + j) * 1024);
             const f32x4 fb = *reinterpret_cast<const f32x4*>(f), fp = *reinterpret_cast<const f32x4*>(f + 64);
             float v[4];
             if constexpr (Cf::DIRECT) {
                 const bf16x4 x = lds_read_tr4(reinterpret_cast<const bf16*>(buf + Cf::v) +
-                                              (tr0 + (l >> 2)) * (16 * NS) + 16 * cg + 4 * (l & 3));
+                                              (tr0 + (l >> 2)) * 16 + 4 * (l & 3));
 #pragma unroll
                 for (int r = 0; r < 4; ++r) v[r] = (float)x[r];
             } else {
 #pragma unroll
                 for (int r = 0; r < 4; ++r) v[r] = vnext[r];
             }
+#pragma unroll
+            for (int kb = 0; kb < 2; ++kb)
+#pragma unroll
+                for (int j = 0; j < WP; ++j)
+                    t8[kb][j] = *reinterpret_cast<const bf16x8*>(tb + (low_block(w, kb < nb ? kb : 0) * WP + j) * 1024);
 #pragma unroll
             for (int kb = 0; kb < KB; ++kb) mma_planes<KP, WP, WP>(k8[kb], s8[kb], P);
             f32x4 R;
@@ -427,6 +429,12 @@ __global__ __launch_bounds__(64 * (6 * NS + 1)) void delta_walk_kernel(const Del
         __syncthreads();
         // U = T R
         f32x4 U = fz;
+        bf16x8 r8[2][WP];
+#pragma unroll
+        for (int kb = 0; kb < 2; ++kb)
+            if (kb < nb)
+#pragma unroll
+                for (int j = 0; j < WP; ++j) r8[kb][j] = *reinterpret_cast<const bf16x8*>(ex + Cf::r + (2 * j + kb) * 1024);
         bf16x8 kt[TI][2][KP];
 #pragma unroll
         for (int i = 0; i < TI; ++i)
@@ -442,12 +450,7 @@ __global__ __launch_bounds__(64 * (6 * NS + 1)) void delta_walk_kernel(const Del
             }
 #pragma unroll
         for (int kb = 0; kb < 2; ++kb)
-            if (kb < nb) {
-                bf16x8 r8[WP];
-#pragma unroll
-                for (int j = 0; j < WP; ++j) r8[j] = *reinterpret_cast<const bf16x8*>(ex + Cf::r + (2 * j + kb) * 1024);
-                mma_planes<WP, WP, WP>(t8[kb], r8, U);
-            }
+            if (kb < nb) mma_planes<WP, WP, WP>(t8[kb], r8[kb], U);
         {
             f32x4 u2;
 #pragma unroll
@@ -499,6 +502,13 @@ __global__ __launch_bounds__(64 * (6 * NS + 1)) void delta_walk_kernel(const Del
     }
 }
 
+template <typename IO, int N>
+__global__ __launch_bounds__(64 * 7) void delta_walk_kernel(const DeltaParams p)
+{
+    extern __shared__ __attribute__((aligned(16))) char wlds[];
+    delta_walk<IO, N, false>(p, nullptr, nullptr, blockIdx.x, wlds);
+}
+
 template <typename F> hipError_t delta_allow_lds(F* kern, size_t bytes)
 {
     const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(kern), hipFuncAttributeMaxDynamicSharedMemorySize,
@@ -507,18 +517,17 @@ template <typename F> hipError_t delta_allow_lds(F* kern, size_t bytes)
     return e;
 }
 
-template <typename IO, int N, int NS, bool TRAIN>
-hipError_t launch_delta_walk(const DeltaParams& p, float* Sbuf, float* Ubuf, hipStream_t stream)
+template <typename IO, int N>
+hipError_t launch_delta_walk(const DeltaParams& p, hipStream_t stream)
 {
-    auto* const kern = &delta_walk_kernel<IO, N, NS, TRAIN>;
-    constexpr size_t lds = WalkCfg<IO, N, NS>::total;
-    static_assert(lds <= 160 * 1024, "a workgroup's LDS");
-    static const hipError_t attr = delta_allow_lds(kern, lds);
+    using Cf = WalkCfg<IO, N, false>;
+    auto* const kern = &delta_walk_kernel<IO, N>;
+    static_assert(Cf::total <= 160 * 1024, "a workgroup's LDS");
+    static const hipError_t attr = delta_allow_lds(kern, Cf::total);
     if (attr != hipSuccess) return attr;
-    const int64_t units = ((int64_t)p.rows * p.H + 7) / 8 * 8;
-    const int64_t blocks = units * (p.P / (16 * NS));
-    constexpr int threads = 64 * WalkCfg<IO, N, NS>::waves;
-    hipLaunchKernelGGL(kern, dim3((unsigned)blocks), dim3(threads), lds, stream, p, Sbuf, Ubuf);
+    const int64_t blocks = ((int64_t)p.rows * p.H + 7) / 8 * 8 * (p.P / 16);
+    const size_t lds = Cf::total;
+    hipLaunchKernelGGL(kern, dim3((unsigned)blocks), dim3(64 * Cf::waves), lds, stream, p);
     return hipGetLastError();
 }
 
