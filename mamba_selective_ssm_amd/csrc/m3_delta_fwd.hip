@@ -1,6 +1,6 @@
 // Gated delta rule, prefill: chunk matrices, then the walk over the chunks.
 #include "m3_delta_chunk.hpp"
-#include "m3_delta_walk.hpp"
+#include "m3_delta_wide.hpp"
 
 namespace m3 {
 
@@ -11,6 +11,13 @@ hipError_t fwd_n(const DeltaParams& p, hipStream_t stream)
 {
     const hipError_t e = launch_delta_chunks<IO, N, false>(p, nullptr, nullptr, stream);
     if (e != hipSuccess) return e;
+    if constexpr (sizeof(IO) == 2) {
+        if ((int64_t)p.rows * p.H * (p.P / 16) > 256) {
+            if constexpr (N < 128)
+                if (p.P % 64 == 0) return launch_delta_wide<N, 4>(p, stream);
+            return launch_delta_wide<N, 2>(p, stream);
+        }
+    }
     return launch_delta_walk<IO, N>(p, stream);
 }
 

@@ -1,0 +1,306 @@
+// Gated delta rule: the walk for calls with more (row, head, 16 columns) than
+// the chip has CUs.
+#pragma once
+
+#include "m3_delta_walk.hpp"
+
+namespace m3 {
+
+// As delta_walk, for 16 NS columns to a workgroup, and with one state
+// wavefront to 16 columns instead of four.  It runs the whole chain in its own
+// registers: with the row order of tile_row a product's result is the next
+// one's second operand as it lies, so neither LDS nor a barrier stands between
+// the products.  A step takes it longer than four wavefronts together (four
+// times their products), but it reads a quarter of what they read from LDS,
+// which is what bounds a CU that runs several of them, and one K, T and
+// set of factors serves NS of them.  The state waves leave the planes of S and U
+// for four output waves, which work one chunk behind, each on one row tile of
+// all column groups, so that Q and A are read once; one barrier a chunk.  bf16
+// calls only: K's planes of a float32 call would leave no room.
+template <int N, int NS> struct WideCfg {
+    static constexpr int WP = DeltaPlanes<bf16>::wide, OP = DeltaPlanes<bf16>::out;
+    static constexpr int KB = N / 32, NT = N / 16, waves = NS + 5;
+    // bytes of one of two buffers, then per column group the planes of S and U, twice
+    static constexpr int k = 0, t = k + 64 * N * 2, f = t + kTriBlocks * WP * 1024, v = f + 5 * 256, buf = v + 64 * NS * 32;
+    static constexpr int ex = 2 * buf, u = OP * KB * 1024, ex1 = u + OP * 2048, total = ex + 2 * NS * ex1;
+};
+
+template <int N, int NS>
+__global__ __launch_bounds__(64 * (NS + 5)) void delta_wide_kernel(const DeltaParams p)
+{
+    using Cf = WideCfg<N, NS>;
+    constexpr int WP = Cf::WP, OP = Cf::OP, KB = Cf::KB, NT = Cf::NT;
+    extern __shared__ __attribute__((aligned(16))) char wlds[];
+
+    const int tid = threadIdx.x, lane = tid & 63, l = lane & 15, g = lane >> 4;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    // the workgroups of one (row, head) run on one XCD and share its L2
+    const int nsl = p.P / (16 * NS);
+    const int64_t idx = blockIdx.x >> 3;
+    const int64_t unit = (idx / nsl) * 8 + (blockIdx.x & 7);
+    if (unit >= (int64_t)p.rows * p.H) return;
+    int64_t b64, h64;
+    split_bh(unit, p.H, b64, h64);
+    const int b = (int)b64, h = (int)h64;
+    const int p0 = (int)(idx % nsl) * (16 * NS);
+    const DeltaRow row = delta_row(p, b);
+    const int64_t rec = delta_record(p, b, tid, 64 * Cf::waves, reinterpret_cast<int*>(wlds));
+    const int nch = (int)((row.len + kDC - 1) / kDC);
+    const int rs = p.G * N, vs = p.H * p.P;
+    const int64_t ci0 = row.slot0 * p.H + h;
+    const int nlast = (int)(row.len - (int64_t)(nch - 1) * kDC);   // tokens of the last chunk
+    const f32x4 fz = {0.f, 0.f, 0.f, 0.f};
+
+    if (wave == NS + 4) {   // loader: chunk c + 1 beside chunk c
+        const bf16* kp = reinterpret_cast<const bf16*>(p.k) + (row.start * p.G + h / (p.H / p.G)) * N;
+        const bf16* vp = reinterpret_cast<const bf16*>(p.v) + (row.start * p.H + h) * p.P + p0;
+        auto stage = [&](int c) {
+            char* buf = wlds + (c & 1) * Cf::buf;
+            const int end = c == nch - 1 ? nlast - 1 : kDC - 1;   // last row to read
+            const bf16 *kc = kp + (int64_t)c * kDC * rs, *vc = vp + (int64_t)c * kDC * vs;
+            const float* fsrc = p.sc + (ci0 + (int64_t)c * p.H) * (kDScal * 64);
+            to_lds16(buf + Cf::f, fsrc + 4 * lane);
+            to_lds4(buf + Cf::f + 1024, fsrc + 256 + lane);
+            constexpr int RPL = 512 / N, VPL = 32 / NS;   // K, V rows of one load
+#pragma unroll
+            for (int i = 0; i < 64 / RPL; ++i) {
+                const int t = RPL * i + lane / (N / 8), j = k_block<N>(t, lane % (N / 8));
+                to_lds16(buf + Cf::k + 1024 * i, kc + (t < end ? t : end) * rs + 8 * j);
+            }
+#pragma unroll
+            for (int i = 0; i < 2 * NS; ++i) {
+                const int t = VPL * i + lane / (2 * NS);
+                to_lds16(buf + Cf::v + 1024 * i, vc + (t < end ? t : end) * vs + 8 * (lane % (2 * NS)));
+            }
+            const char* tsrc = reinterpret_cast<const char*>(p.tf + (ci0 + (int64_t)c * p.H) * (kTriBlocks * WP * 512));
+#pragma unroll
+            for (int i = 0; i < kTriBlocks * WP; ++i) to_lds16(buf + Cf::t + 1024 * i, tsrc + 1024 * i + 16 * lane);
+        };
+        auto barrier = [&]() {
+            asm volatile("" ::: "memory");
+            __builtin_amdgcn_s_waitcnt(0);
+            __builtin_amdgcn_s_barrier();
+            asm volatile("" ::: "memory");
+        };
+        if (nch > 0) stage(0);
+        barrier();
+        for (int c = 0; c < nch; ++c) {
+            if (c + 1 < nch) stage(c + 1);
+            barrier();
+        }
+        return;
+    }
+
+    if (wave >= NS) {   // output: row tile w of chunk c beside the state's chunk c + 1, as O^T
+        // (NB: 32-token blocks that the tile of A spans.)  No load depends on a
+        // branch: where one might, a wait for the chunk's operands would also
+        // wait for those of the chunk after it.
+        auto output = [&](auto blocks) {
+            constexpr int NB = decltype(blocks)::value;
+            const int w = wave - NS;
+            const int t = tile_row(w, l);   // this lane's token
+            const bf16* qp = reinterpret_cast<const bf16*>(p.q) + (row.start * p.G + h / (p.H / p.G)) * N + 8 * g;
+            bf16* op = reinterpret_cast<bf16*>(p.o) + (row.start * p.H + h) * p.P + p0 + 4 * g;
+            bf16x8 q[KB][1], a[NB][OP];
+            float fo;
+            auto load = [&](int c) {
+                c = c < nch ? c : nch - 1;
+                const int end = c == nch - 1 ? nlast - 1 : kDC - 1;
+                const bf16* qc = qp + (int64_t)c * kDC * rs + (t < end ? t : end) * rs;
+#pragma unroll
+                for (int kb = 0; kb < KB; ++kb) q[kb][0] = *reinterpret_cast<const bf16x8*>(qc + 32 * kb);
+                const bf16* src = p.af + (ci0 + (int64_t)c * p.H) * (kTriBlocks * OP * 512) + lane * 8;
+#pragma unroll
+                for (int kb = 0; kb < NB; ++kb)
+#pragma unroll
+                    for (int j = 0; j < OP; ++j)
+                        a[kb][j] = *reinterpret_cast<const bf16x8*>(src + (low_block(w, kb) * OP + j) * 512);
+                fo = p.sc[(ci0 + (int64_t)c * p.H) * (kDScal * 64) + 192 + t];
+            };
+            if (nch > 0) load(0);
+            __syncthreads();
+            for (int c = 0; c < nch; ++c) {
+                __syncthreads();   // the state waves are done with chunk c
+                const char* ex = wlds + Cf::ex + (c & 1) * Cf::ex1 + 16 * lane;
+                f32x4 acc[NS];
+#pragma unroll
+                for (int i = 0; i < NS; ++i) {
+                    const char* e = ex + i * 2 * Cf::ex1;
+                    acc[i] = fz;
+#pragma unroll
+                    for (int kb = 0; kb < KB; ++kb) {
+                        bf16x8 s8[1][OP];
+#pragma unroll
+                        for (int j = 0; j < OP; ++j) s8[0][j] = *reinterpret_cast<const bf16x8*>(e + (j * KB + kb) * 1024);
+                        mma_tiles<1, OP, 1, OP>(s8, q[kb], &acc[i]);
+                    }
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) acc[i][r] *= fo;
+#pragma unroll
+                    for (int kb = 0; kb < NB; ++kb) {
+                        bf16x8 u8[1][OP];
+#pragma unroll
+                        for (int j = 0; j < OP; ++j) u8[0][j] = *reinterpret_cast<const bf16x8*>(e + Cf::u + (2 * j + kb) * 1024);
+                        mma_tiles<1, OP, OP, OP>(u8, a[kb], &acc[i]);
+                    }
+                }
+                load(c + 1);
+                if (t < (c == nch - 1 ? nlast : kDC)) {
+                    bf16* oc = op + ((int64_t)c * kDC + t) * vs;
+#pragma unroll
+                    for (int i = 0; i < NS; ++i) gstore4(oc + 16 * i, acc[i]);
+                }
+            }
+        };
+        if (wave < NS + 2) output(std::integral_constant<int, 1>());
+        else output(std::integral_constant<int, 2>());
+        return;
+    }
+
+    const int cg = wave;   // column group
+    char* ex0 = wlds + Cf::ex + cg * 2 * Cf::ex1 + 16 * lane;
+
+    // state: tile i holds rows tile_row(i, 4 g + r) of the state, column l
+    const int col = p0 + 16 * cg + l;
+    f32x4 S[NT];
+    const float* hin = p.h_in != nullptr && rec >= 0 ? p.h_in + ((rec * p.H + h) * N + 8 * g) * p.P + col : nullptr;
+#pragma unroll
+    for (int i = 0; i < NT; ++i)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+            S[i][r] = hin != nullptr ? hin[(32 * (i >> 1) + 4 * (i & 1) + r) * p.P] : 0.f;
+            if (rec == -2) S[i][r] = __builtin_nanf("");   // the record belongs to an earlier row
+        }
+    auto planes_of = [&](const f32x4& x, const f32x4& y, bf16x8 (&o)[WP]) {
+        bf16x4 lo[WP], hi[WP];
+        to_planes4<WP>(x, lo);
+        to_planes4<WP>(y, hi);
+#pragma unroll
+        for (int j = 0; j < WP; ++j) o[j] = join8(lo[j], hi[j]);
+    };
+    bf16x8 s8[KB][WP];
+#pragma unroll
+    for (int kb = 0; kb < KB; ++kb) planes_of(S[2 * kb], S[2 * kb + 1], s8[kb]);
+    __syncthreads();
+
+    for (int c = 0; c < nch; ++c) {
+        const char* buf = wlds + (c & 1) * Cf::buf;
+        char* ex = ex0 + (c & 1) * Cf::ex1;
+#pragma unroll
+        for (int kb = 0; kb < KB; ++kb)
+#pragma unroll
+            for (int j = 0; j < OP; ++j) *reinterpret_cast<bf16x8*>(ex + (j * KB + kb) * 1024) = s8[kb][j];
+        // R = beta V - sp (K S)
+        f32x4 P[4] = {fz, fz, fz, fz};
+#pragma unroll
+        for (int kb = 0; kb < KB; ++kb) {
+            bf16x8 k8[4][1];
+#pragma unroll
+            for (int rt = 0; rt < 4; ++rt) {
+                const int t = tile_row(rt, l);
+                k8[rt][0] = *reinterpret_cast<const bf16x8*>(buf + Cf::k + t * (2 * N) + 16 * k_block<N>(t, 4 * kb + g));
+            }
+            mma_tiles<4, 1, WP, WP>(k8, s8[kb], P);
+        }
+        bf16x8 r8[2][WP];
+        const float* f = reinterpret_cast<const float*>(buf + Cf::f) + 8 * g;
+#pragma unroll
+        for (int rt = 0; rt < 4; ++rt) {
+            const int t0 = 32 * (rt >> 1) + 4 * (rt & 1);
+            const f32x4 fb = *reinterpret_cast<const f32x4*>(f + t0), fp = *reinterpret_cast<const f32x4*>(f + 64 + t0);
+            const bf16x4 v = lds_read_tr4(reinterpret_cast<const bf16*>(buf + Cf::v) + (t0 + 8 * g + (l >> 2)) * (16 * NS) +
+                                          16 * cg + 4 * (l & 3));
+#pragma unroll
+            for (int r = 0; r < 4; ++r) P[rt][r] = fb[r] * (float)v[r] - fp[r] * P[rt][r];
+        }
+        planes_of(P[0], P[1], r8[0]);
+        planes_of(P[2], P[3], r8[1]);
+        // U = T R
+        f32x4 U[4] = {fz, fz, fz, fz};
+        {
+            const char* tb = buf + Cf::t + 16 * lane;
+            bf16x8 t4[4][WP], t2[2][WP];
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int j = 0; j < WP; ++j) t4[i][j] = *reinterpret_cast<const bf16x8*>(tb + (i * WP + j) * 1024);
+            mma_tiles<4, WP, WP, WP>(t4, r8[0], U);
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+#pragma unroll
+                for (int j = 0; j < WP; ++j) t2[i][j] = *reinterpret_cast<const bf16x8*>(tb + ((4 + i) * WP + j) * 1024);
+            mma_tiles<2, WP, WP, WP>(t2, r8[1], U + 2);
+        }
+#pragma unroll
+        for (int kb = 0; kb < 2; ++kb) {
+            bf16x4 lo[OP], hi[OP];
+            to_planes4<OP>(U[2 * kb], lo);
+            to_planes4<OP>(U[2 * kb + 1], hi);
+#pragma unroll
+            for (int j = 0; j < OP; ++j) *reinterpret_cast<bf16x8*>(ex + Cf::u + (2 * j + kb) * 1024) = join8(lo[j], hi[j]);
+        }
+#pragma unroll
+        for (int rt = 0; rt < 4; ++rt) {
+            const f32x4 fu = *reinterpret_cast<const f32x4*>(f + 128 + 32 * (rt >> 1) + 4 * (rt & 1));
+#pragma unroll
+            for (int r = 0; r < 4; ++r) U[rt][r] *= fu[r];
+        }
+        planes_of(U[0], U[1], r8[0]);
+        planes_of(U[2], U[3], r8[1]);
+        // S <- e^G_last S + K^T (d U)
+        const float eL = *reinterpret_cast<const float*>(buf + Cf::f + 1024 + 4 * lane);
+        constexpr int TN = NT < 4 ? NT : 4;   // tiles in turn
+#pragma unroll
+        for (int i0 = 0; i0 < NT; i0 += TN) {
+            f32x4 acc[TN];
+#pragma unroll
+            for (int i = 0; i < TN; ++i) acc[i] = fz;
+#pragma unroll
+            for (int kb = 0; kb < 2; ++kb) {
+                bf16x8 kt[TN][1];
+                const int t = 32 * kb + 8 * g + (l >> 2);
+#pragma unroll
+                for (int i = 0; i < TN; ++i) {
+                    const int j4 = 4 * ((i0 + i) >> 1) + (l & 3);
+                    const char* src = buf + Cf::k + 8 * (i & 1);
+                    kt[i][0] = join8(lds_read_tr4(reinterpret_cast<const bf16*>(src + t * (2 * N) + 16 * k_block<N>(t, j4))),
+                                     lds_read_tr4(reinterpret_cast<const bf16*>(src + (t + 4) * (2 * N) + 16 * k_block<N>(t + 4, j4))));
+                }
+                mma_tiles<TN, 1, WP, WP>(kt, r8[kb], acc);
+            }
+#pragma unroll
+            for (int i = 0; i < TN; i += 2) {
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    S[i0 + i][r] = eL * S[i0 + i][r] + acc[i][r];
+                    S[i0 + i + 1][r] = eL * S[i0 + i + 1][r] + acc[i + 1][r];
+                }
+                planes_of(S[i0 + i], S[i0 + i + 1], s8[(i0 + i) / 2]);
+            }
+        }
+        __syncthreads();
+    }
+    if (p.h_out != nullptr && rec >= 0) {
+        float* ho = p.h_out + ((rec * p.H + h) * N + 8 * g) * p.P + col;
+#pragma unroll
+        for (int i = 0; i < NT; ++i)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) ho[(32 * (i >> 1) + 4 * (i & 1) + r) * p.P] = S[i][r];
+    }
+}
+
+template <int N, int NS>
+hipError_t launch_delta_wide(const DeltaParams& p, hipStream_t stream)
+{
+    using Cf = WideCfg<N, NS>;
+    auto* const kern = &delta_wide_kernel<N, NS>;
+    static_assert(Cf::total <= 160 * 1024, "a workgroup's LDS");
+    static const hipError_t attr = delta_allow_lds(kern, Cf::total);
+    if (attr != hipSuccess) return attr;
+    const int64_t blocks = ((int64_t)p.rows * p.H + 7) / 8 * 8 * (p.P / (16 * NS));
+    const size_t lds = Cf::total;
+    hipLaunchKernelGGL(kern, dim3((unsigned)blocks), dim3(64 * Cf::waves), lds, stream, p);
+    return hipGetLastError();
+}
+
+}  // namespace m3

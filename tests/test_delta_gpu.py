@@ -72,6 +72,40 @@ def test_prefill(B, L, H, G, N, P, io, l2):
         check_h(hL, wh, "zero state" if h0 is None else "given state")
 
 
+@pytest.mark.parametrize("N,P", [(32, 32), (32, 64), (64, 96), (64, 64), (128, 64), (128, 128)])
+def test_many_heads(N, P):
+    """More (row, head, 16 columns) than CUs; packed sequences of all lengths
+    around a chunk's, in a pool, some without a record, one slot named twice."""
+    H = 4600 // P
+    lens = [1, 130, 64, 0, 63, 200, 17, 65]
+    x = ref.inputs(1, sum(lens), H, H, N, P, torch.bfloat16, 15)
+    pool = torch.randn(9, H, N, P, generator=torch.Generator().manual_seed(16)).cuda()
+    before = pool.clone()
+    sl = torch.tensor([8, 0, 3, 5, -1, 2, 0, 6], dtype=torch.int32, device="cuda")
+    cu = torch.tensor([0] + lens).cumsum(0).to(torch.int32).cuda()
+    assert len(lens) * H * P // 16 > 256
+    o, _ = m3_delta_fwd(*x, pool, l2norm=True, scale=0.2, cu_seqlens=cu, max_seqlen=200, slots=sl)
+    start = torch.stack([before[s] if s >= 0 else torch.zeros_like(before[0]) for s in sl.tolist()])
+    want = ref.packed(ref.forward, lens, x, [start], scale=0.2, l2norm=True)
+    at = 0
+    for i, n in enumerate(lens):
+        if i == 6:
+            assert bool(o[:, at:at + n].isnan().all())
+        elif n:
+            check_o(o[:, at:at + n], want[i][0], "bf16", "row %d" % i)
+        if i not in (4, 6):
+            check_h(pool[sl[i].item()][None], want[i][1], "row %d" % i)
+        at += n
+    for s in (1, 4, 7):
+        assert torch.equal(pool[s], before[s])
+    # a dense batch without a state, one row longer than the others would be
+    y = ref.inputs(8, 70, H, 1, N, P, torch.bfloat16, 17)
+    o, h = m3_delta_fwd(*y, l2norm=True, scale=0.2)
+    wo, wh = ref.forward(*y, scale=0.2, l2norm=True)
+    check_o(o, wo, "bf16", "dense")
+    check_h(h, wh, "dense")
+
+
 def test_default_scale_and_no_state():
     x = ref.inputs(1, 70, 2, 2, 64, 32, torch.bfloat16, 21)
     o, h = m3_delta_fwd(*x, l2norm=True, return_state=False)
