@@ -80,17 +80,22 @@ def packer(cls):
 _pack_fwd, _pack_step, _pack_bwd = packer(DeltaArgs), packer(DeltaStepArgs), packer(DeltaBwdArgs)
 
 
+# The handle alone: building a Stream object around it takes 2.7 of a one-token
+# step's 12 us.
+_current_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+    (lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
 def enter(device, stream):
     """The handle of the stream that a call on `device` runs on (None: the
     device's current stream), and the contexts that make that device and
     stream current, which the call's own allocations follow (None: they are)."""
-    here = torch.cuda.current_device()
-    if stream is None and here == device.index:
-        return torch.cuda.current_stream().cuda_stream, None
+    if stream is None and torch.cuda.current_device() == device.index:
+        return _current_stream(device.index), None
     ctx = contextlib.ExitStack()
     ctx.enter_context(torch.cuda.device(device))
     if stream is None:
-        return torch.cuda.current_stream().cuda_stream, ctx
+        return _current_stream(device.index), ctx
     if stream.device != device:
         ctx.close()
         raise ValueError("stream belongs to %s, the tensors to %s" % (stream.device, device))
