@@ -57,8 +57,6 @@ struct DeltaBwdParams {
     const void* dout;
     const float* dh_out;
     float *dq, *dk, *dv, *dg, *dbeta, *dh_in;
-    bf16* ttf;             // T^T in operand order
-    bf16* atf;             // A^T in operand order
     float* S;              // [chunk][N][P] state before each chunk
     float* dS;             // [chunk][N][P] adjoint of the state after each chunk
     float* U;              // [chunk][64][P]
@@ -91,11 +89,9 @@ template <> struct DeltaPlanes<float> { static constexpr int io = 3, wide = 3, o
 __host__ __device__ constexpr int tile_row(int i, int m) { return 32 * (i >> 1) + 8 * (m >> 2) + 4 * (i & 1) + (m & 3); }
 
 // Operand blocks of a lower triangular 64 x 64 matrix, 16 rows (of tile w) x 32
-// columns each, in the order (0,0) (1,0) (2,0) (3,0) (2,1) (3,1) of (w, kb); of
-// an upper triangular one (the transposes) (0,0) (1,0) (0,1) (1,1) (2,1) (3,1).
+// columns each, in the order (0,0) (1,0) (2,0) (3,0) (2,1) (3,1) of (w, kb).
 constexpr int kTriBlocks = 6;
 __host__ __device__ constexpr int low_block(int w, int kb) { return w + 2 * kb; }
-__host__ __device__ constexpr int up_block(int w, int kb) { return w + 2 * kb; }
 
 inline size_t delta_tri_elems(int planes) { return (size_t)kTriBlocks * planes * 512; }
 

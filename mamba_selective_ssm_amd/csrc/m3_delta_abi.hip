@@ -80,7 +80,7 @@ m3_status plan_delta(const m3_delta_args* a, DeltaPlan* out)
     const size_t tokens = (size_t)(packed ? 1 : a->batch) * (size_t)a->seqlen;
     out->heads = out->G == H ? 0 : up256(tokens * (size_t)(H * a->dstate) * 4);
     out->fwd = n == 0 ? 0 : out->tri_w + out->tri_o + out->sc;
-    out->bwd = n == 0 ? 0 : 3 * out->tri_w + out->sc + 2 * out->st + 2 * out->rowsP + 2 * out->heads;
+    out->bwd = n == 0 ? 0 : out->tri_w + out->sc + 2 * out->st + 2 * out->rowsP + 2 * out->heads;
     return M3_OK;
 }
 
@@ -328,8 +328,6 @@ m3_status m3_delta_bwd(const m3_delta_bwd_args* b, void* stream)
     char* w = static_cast<char*>(a->workspace);
     auto take = [&w](size_t bytes) { char* x = w; w += bytes; return x; };
     p.f.tf = reinterpret_cast<m3::bf16*>(take(pl.tri_w));
-    p.ttf = reinterpret_cast<m3::bf16*>(take(pl.tri_w));
-    p.atf = reinterpret_cast<m3::bf16*>(take(pl.tri_w));
     p.f.sc = reinterpret_cast<float*>(take(pl.sc));
     p.S = reinterpret_cast<float*>(take(pl.st));
     p.dS = reinterpret_cast<float*>(take(pl.st));

@@ -21,17 +21,33 @@
 
 namespace m3 {
 
-// E1 = A^T dO (left where dR goes) and E2 = Q^T (so dO) (where dS goes).  One
-// workgroup per chunk and head: wave w takes row tile w of E1 and the state
-// tiles w, w + 4 of E2, all columns.  Bound by what it writes (4 (64 + N) P
-// bytes a chunk).
-template <typename IO, int N>
+// Sum over the four lane groups (g).
+__device__ __forceinline__ float groups_sum(float v)
+{
+    v += __shfl_xor(v, 16);
+    v += __shfl_xor(v, 32);
+    return v;
+}
+
+// E1 = A^T dO (left where dR goes) and E2 = Q^T (so dO) (where dS goes), both
+// made as their transposes, so that a lane stores four neighbours.  One
+// workgroup per chunk and head: wave w takes tokens 16 w .. + 15 of E1 and rows
+// 16 w .. (and 16 w + 64 ..) of E2, all columns.  A comes out of Q K^T as the
+// second operand.  Bound by memory: it reads a chunk's K, Q and dO and writes
+// 4 (64 + N) P bytes.
+template <typename IO, int N, int PB> struct PreCfg {
+    static constexpr int KP = DeltaPlanes<IO>::io, LQ = N + 8, LO = 32 * PB + 8;
+    static constexpr int q = KP * 64 * LQ * 2, o = 2 * q, f = o + KP * 64 * LO * 2, total = f + 4 * 64 * 4;
+};
+template <typename IO, int N, int PB>
 __global__ __launch_bounds__(256) void delta_pre_kernel(const DeltaBwdParams bp)
 {
+    using Cf = PreCfg<IO, N, PB>;
     const DeltaParams& p = bp.f;
-    constexpr int KP = DeltaPlanes<IO>::io, WP = DeltaPlanes<IO>::wide, NT = N / 16, TI = (NT + 3) / 4, LQ = N + 8, LO = 136;
-    __shared__ __attribute__((aligned(16))) bf16 sQ[KP * 64 * LQ];
-    __shared__ __attribute__((aligned(16))) bf16 sO[KP * 64 * LO];
+    constexpr int KP = Cf::KP, WP = DeltaPlanes<IO>::wide, NT = N / 16, TI = (NT + 3) / 4, LQ = Cf::LQ, LO = Cf::LO, P = 32 * PB;
+    extern __shared__ __attribute__((aligned(16))) char plds[];
+    bf16 *sK = reinterpret_cast<bf16*>(plds), *sQ = reinterpret_cast<bf16*>(plds + Cf::q), *sO = reinterpret_cast<bf16*>(plds + Cf::o);
+    float* sF = reinterpret_cast<float*>(plds + Cf::f);   // 1/|k|, G's two parts, 1/|q|
     const int tid = threadIdx.x, lane = tid & 63, l = lane & 15, g = lane >> 4;
     const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int64_t bid = blockIdx.x;
@@ -41,72 +57,120 @@ __global__ __launch_bounds__(256) void delta_pre_kernel(const DeltaBwdParams bp)
     if ((int64_t)c * kDC >= row.len) return;
     const int64_t t0 = row.start + (int64_t)c * kDC, ci = (row.slot0 + c) * p.H + h;
     const int nv = row.len - (int64_t)c * kDC < kDC ? (int)(row.len - (int64_t)c * kDC) : kDC;
-    const IO* qp = reinterpret_cast<const IO*>(p.q) + (t0 * p.G + h / (p.H / p.G)) * N;
-    const IO* op = reinterpret_cast<const IO*>(bp.dout) + (t0 * p.H + h) * p.P;
-    const int rs = p.G * N, vs = p.H * p.P, P = p.P;
+    const int hg = h / (p.H / p.G);
+    const IO* qp = reinterpret_cast<const IO*>(p.q) + (t0 * p.G + hg) * N;
+    const IO* kp = reinterpret_cast<const IO*>(p.k) + (t0 * p.G + hg) * N;
+    const IO* op = reinterpret_cast<const IO*>(bp.dout) + (t0 * p.H + h) * P;
+    const int rs = p.G * N, vs = p.H * P;
+    const f32x4 fz = {0.f, 0.f, 0.f, 0.f};
 
     // rows past the end are zero
-    for (int i = tid; i < 64 * N / 8; i += 256) {
-        const int t = i / (N / 8), j = i % (N / 8);
-        RawRow8<IO> x;
-        x.load(qp + (t < nv ? t : 0) * rs + 8 * j, t < nv);
-        bf16x8 o[KP];
-        x.planes(o);
+    auto put = [&](const IO* src, int stride, int width, bf16* dst, int ld) {
+        for (int i = tid; i < 8 * width; i += 256) {
+            const int t = i / (width / 8), j = i % (width / 8);
+            RawRow8<IO> x;
+            x.load(src + (t < nv ? t : 0) * stride + 8 * j, t < nv);
+            bf16x8 o[KP];
+            x.planes(o);
 #pragma unroll
-        for (int e = 0; e < KP; ++e) *reinterpret_cast<bf16x8*>(sQ + (e * 64 + t) * LQ + 8 * j) = o[e];
-    }
-    for (int i = tid; i < 8 * P; i += 256) {
-        const int t = i / (P / 8), j = i % (P / 8);
-        RawRow8<IO> x;
-        x.load(op + (t < nv ? t : 0) * vs + 8 * j, t < nv);
-        bf16x8 o[KP];
-        x.planes(o);
-#pragma unroll
-        for (int e = 0; e < KP; ++e) *reinterpret_cast<bf16x8*>(sO + (e * 64 + t) * LO + 8 * j) = o[e];
-    }
-    // A^T's rows of this wave: 32-token blocks w / 2 .. 1
-    bf16x8 at[2][WP];
-    const bf16* ap = bp.atf + ci * (kTriBlocks * WP * 512) + lane * 8;
-#pragma unroll
-    for (int kb = 0; kb < 2; ++kb)
-#pragma unroll
-        for (int j = 0; j < WP; ++j)
-            at[kb][j] = *reinterpret_cast<const bf16x8*>(ap + (up_block(w, kb < (w >> 1) ? 1 : kb) * WP + j) * 512);
-    const float* f = p.sc + ci * (kDScal * 64) + 192;
-    float so[2][8];
-#pragma unroll
-    for (int kb = 0; kb < 2; ++kb)
-#pragma unroll
-        for (int e = 0; e < 8; ++e) so[kb][e] = f[32 * kb + 8 * g + e];
+            for (int e = 0; e < KP; ++e) *reinterpret_cast<bf16x8*>(dst + (e * 64 + t) * ld + 8 * j) = o[e];
+        }
+    };
+    put(kp, rs, N, sK, LQ);
+    put(qp, rs, N, sQ, LQ);
+    put(op, vs, P, sO, LO);
+    if (tid < 192) sF[tid] = p.sc[ci * (kDScal * 64) + 320 + tid];
     __syncthreads();
-    // Q^T's rows of this wave
-    bf16x8 qt[TI][2][KP];
+    {
+        const int t = 16 * w + l;
+        float q2 = 0.f;
+#pragma unroll
+        for (int j = 0; j < N / 32; ++j)
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                float x = 0.f;
+#pragma unroll
+                for (int k = KP - 1; k >= 0; --k) x += (float)sQ[(k * 64 + t) * LQ + 32 * j + 8 * g + e];
+                q2 += x * x;
+            }
+        q2 = groups_sum(q2);
+        if (g == 0) sF[192 + t] = t >= nv ? 0.f : p.l2norm ? __builtin_amdgcn_rsqf(q2 + p.eps) : 1.f;
+    }
+    __syncthreads();
+
+    // A's column of this lane's token j as the second operand: rows 32 kb + 8 g ..
+    bf16x8 at[2][WP];
+    {
+        const int j = 16 * w + l;
+        const float rk = sF[j], gh = sF[64 + j], gl = sF[128 + j];
+        bf16x8 k8[N / 32][KP];
+#pragma unroll
+        for (int kn = 0; kn < N / 32; ++kn)
+#pragma unroll
+            for (int e = 0; e < KP; ++e) k8[kn][e] = *reinterpret_cast<const bf16x8*>(sK + (e * 64 + j) * LQ + 32 * kn + 8 * g);
+#pragma unroll
+        for (int kb = 0; kb < 2; ++kb) {
+#pragma unroll
+            for (int e = 0; e < WP; ++e) at[kb][e] = zero8();
+            if (kb < (w >> 1)) continue;   // wave-uniform
+            bf16x4 lo[WP], hi[WP];
+#pragma unroll
+            for (int s = 0; s < 2; ++s) {
+                f32x4 qk = fz;
+                const int qrow = tile_row(2 * kb + s, l);
+#pragma unroll
+                for (int kn = 0; kn < N / 32; ++kn) {
+                    bf16x8 q8[KP];
+#pragma unroll
+                    for (int e = 0; e < KP; ++e) q8[e] = *reinterpret_cast<const bf16x8*>(sQ + (e * 64 + qrow) * LQ + 32 * kn + 8 * g);
+                    mma_planes<KP, KP, WP>(q8, k8[kn], qk);
+                }
+                const int i0 = 32 * kb + 8 * g + 4 * s;
+                const f32x4 gh4 = *reinterpret_cast<const f32x4*>(sF + 64 + i0), gl4 = *reinterpret_cast<const f32x4*>(sF + 128 + i0);
+                const f32x4 rq4 = *reinterpret_cast<const f32x4*>(sF + 192 + i0);
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    const float D = __builtin_amdgcn_exp2f((gh4[r] - gh) + (gl4[r] - gl)) * rk;
+                    qk[r] = i0 + r >= j ? p.scale * rq4[r] * D * qk[r] : 0.f;
+                }
+                to_planes4<WP>(qk, s == 0 ? lo : hi);
+            }
+#pragma unroll
+            for (int e = 0; e < WP; ++e) at[kb][e] = join8(lo[e], hi[e]);
+        }
+    }
+    // columns of Q, and so of the tokens 32 kb + 8 g ..
     auto tr8 = [&](const bf16* base, int ld, int kb, int col) {
-        const bf16* s = base + (32 * kb + 8 * g + (l >> 2)) * ld + col;
+        const bf16* s = base + (32 * kb + 8 * g + (l >> 2)) * ld + col + 4 * (l & 3);
         return join8(lds_read_tr4(s), lds_read_tr4(s + 4 * ld));
     };
+    bf16x8 qt[TI][2][KP];
+    float so[2][8];
 #pragma unroll
-    for (int i = 0; i < TI; ++i)
+    for (int kb = 0; kb < 2; ++kb) {
 #pragma unroll
-        for (int kb = 0; kb < 2; ++kb)
+        for (int i = 0; i < TI; ++i)
 #pragma unroll
-            for (int e = 0; e < KP; ++e) {
-                const int ti = w + 4 * i < NT ? w + 4 * i : 0;
-                qt[i][kb][e] = tr8(sQ + e * 64 * LQ, LQ, kb, 32 * (ti >> 1) + 8 * (l & 3) + 4 * (ti & 1));
-            }
-    const int tr0 = 32 * (w >> 1) + 4 * (w & 1) + 8 * g;
-    float* e1 = bp.dR + ci * 64 * (int64_t)P;
-    float* e2 = bp.dS + ci * N * (int64_t)P;
+            for (int e = 0; e < KP; ++e) qt[i][kb][e] = tr8(sQ + e * 64 * LQ, LQ, kb, 16 * (w + 4 * i < NT ? w + 4 * i : 0));
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            const int t = 32 * kb + 8 * g + e;
+            so[kb][e] = p.scale * __builtin_amdgcn_exp2f(sF[64 + t] + sF[128 + t]) * sF[192 + t];
+        }
+    }
+    float* e1 = bp.dR + (ci * 64 + 16 * w + l) * (int64_t)P + 4 * g;
+    float* e2 = bp.dS + (ci * N + 16 * w + l) * (int64_t)P + 4 * g;
+#pragma unroll
     for (int pt = 0; pt < P / 16; ++pt) {
-        f32x4 a1 = {0.f, 0.f, 0.f, 0.f}, a2[TI];
+        f32x4 a1 = fz, a2[TI];
 #pragma unroll
-        for (int i = 0; i < TI; ++i) a2[i] = f32x4{0.f, 0.f, 0.f, 0.f};
+        for (int i = 0; i < TI; ++i) a2[i] = fz;
 #pragma unroll
         for (int kb = 0; kb < 2; ++kb) {
             bf16x8 o8[KP], s8[WP];
 #pragma unroll
-            for (int e = 0; e < KP; ++e) o8[e] = tr8(sO + e * 64 * LO, LO, kb, 16 * pt + 4 * (l & 3));
-            if (kb >= (w >> 1)) mma_planes<WP, KP, WP>(at[kb], o8, a1);
+            for (int e = 0; e < KP; ++e) o8[e] = tr8(sO + e * 64 * LO, LO, kb, 16 * pt);
+            if (kb >= (w >> 1)) mma_planes<KP, WP, WP>(o8, at[kb], a1);
 #pragma unroll
             for (int e = 0; e < 8; e += 2) {
                 float x = 0.f, y = 0.f;
@@ -121,15 +185,12 @@ __global__ __launch_bounds__(256) void delta_pre_kernel(const DeltaBwdParams bp)
                 for (int j = 0; j < WP; ++j) { s8[j][e] = t[j][0]; s8[j][e + 1] = t[j][1]; }
             }
 #pragma unroll
-            for (int i = 0; i < TI; ++i) mma_planes<KP, WP, WP>(qt[i][kb], s8, a2[i]);
+            for (int i = 0; i < TI; ++i) mma_planes<WP, KP, WP>(s8, qt[i][kb], a2[i]);
         }
-#pragma unroll
-        for (int r = 0; r < 4; ++r) e1[(tr0 + r) * P + 16 * pt + l] = a1[r];
+        *reinterpret_cast<f32x4*>(e1 + 16 * pt) = a1;
 #pragma unroll
         for (int i = 0; i < TI; ++i)
-            if (w + 4 * i < NT)
-#pragma unroll
-                for (int r = 0; r < 4; ++r) e2[(tr0 + 64 * i + r) * P + 16 * pt + l] = a2[i][r];
+            if (w + 4 * i < NT) *reinterpret_cast<f32x4*>(e2 + 64 * i * P + 16 * pt) = a2[i];
     }
 }
 
@@ -156,7 +217,7 @@ __device__ __forceinline__ void delta_back(const DeltaBwdParams& bp, int64_t bid
     const int64_t ci0 = row.slot0 * p.H + h;
     const int nlast = (int)(row.len - (int64_t)(nch - 1) * kDC);
     if (wave == 4) {
-        walk_loader<IO, N, true, true>(p, wlds, bp.ttf, row, h, p0, nch, nlast, lane);
+        walk_loader<IO, N, true, true>(p, wlds, p.tf, row, h, p0, nch, nlast, lane);
         return;
     }
     char* ex = wlds + Cf::ex + 16 * lane;
@@ -200,7 +261,7 @@ __device__ __forceinline__ void delta_back(const DeltaBwdParams& bp, int64_t bid
         const int64_t ci = ci0 + (int64_t)c * p.H;
         const char* buf = wlds + (s % NBUF) * Cf::buf;
         const float* f = reinterpret_cast<const float*>(buf + Cf::f) + tr0;
-        const char* tb = wlds + Cf::t + (s % Cf::TB) * Cf::tsize + 16 * lane;
+        const char* tb = wlds + Cf::t + (s % Cf::TB) * Cf::tsize + 16 * (16 * (l & 3) + 4 * g + (l >> 2)) + half;
         const f32x4 c1 = e1;
         f32x4 c2[TI];
 #pragma unroll
@@ -234,8 +295,14 @@ __device__ __forceinline__ void delta_back(const DeltaBwdParams& bp, int64_t bid
 #pragma unroll
             for (int kb = 0; kb < 2; ++kb)
 #pragma unroll
-                for (int j = 0; j < WP; ++j)
-                    t8[kb][j] = *reinterpret_cast<const bf16x8*>(tb + (up_block(w, kb < kb0 ? 1 : kb) * WP + j) * 1024);
+                for (int j = 0; j < WP; ++j) {
+                    // rows of T^T: columns tile_row(w, l) of T, rows 32 kb + 8 g ..
+                    // (tiles 2 kb, 2 kb + 1 of T, their column block w / 2)
+                    const int k = kb < kb0 ? 1 : kb;
+                    const char* s = tb + j * 1024;
+                    t8[kb][j] = join8(lds_read_tr4(reinterpret_cast<const bf16*>(s + low_block(2 * k, kb0) * (WP * 1024))),
+                                      lds_read_tr4(reinterpret_cast<const bf16*>(s + low_block(2 * k + 1, kb0) * (WP * 1024))));
+                }
             f32x4 dU;
 #pragma unroll
             for (int r = 0; r < 4; ++r) dU[r] = c1[r] + fu[r] * X[r];
@@ -325,14 +392,6 @@ __global__ __launch_bounds__(320) void delta_walks_kernel(const DeltaBwdParams b
     const unsigned n = gridDim.x / 2;   // a multiple of 8: the XCDs of both halves agree
     if (blockIdx.x < n) delta_back<IO, N>(bp, blockIdx.x, wlds);
     else delta_walk<IO, N, true>(bp.f, bp.S, bp.U, blockIdx.x - n, wlds);
-}
-
-// Sum over the four lane groups (g).
-__device__ __forceinline__ float groups_sum(float v)
-{
-    v += __shfl_xor(v, 16);
-    v += __shfl_xor(v, 32);
-    return v;
 }
 
 template <typename IO, int N, int PB> struct GradCfg {
@@ -714,8 +773,11 @@ __global__ __launch_bounds__(256, PB <= 2 ? 2 : 1) void delta_grad_kernel(const 
 }
 
 // dq and dk of a group of heads: the sum over its heads, in their order.
-static __global__ __launch_bounds__(256) void delta_heads_kernel(const float* e, float* out, int64_t tokens, int H, int G, int N)
+static __global__ __launch_bounds__(256) void delta_heads_kernel(const float* eq, const float* ek, float* oq, float* ok,
+                                                                  int64_t tokens, int H, int G, int N)
 {
+    const float* e = blockIdx.y ? ek : eq;
+    float* out = blockIdx.y ? ok : oq;
     const int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4;
     if (i >= tokens * G * N) return;
     const int64_t t = i / ((int64_t)G * N);
@@ -749,6 +811,20 @@ static __global__ __launch_bounds__(256) void delta_rest_kernel(const DeltaParam
 }
 
 template <typename IO, int N, int PB>
+hipError_t launch_delta_pre(const DeltaBwdParams& bp, hipStream_t stream)
+{
+    auto* const kern = &delta_pre_kernel<IO, N, PB>;
+    constexpr size_t lds = PreCfg<IO, N, PB>::total;
+    static_assert(lds <= 160 * 1024, "a workgroup's LDS");
+    static const hipError_t attr = delta_allow_lds(kern, lds);
+    if (attr != hipSuccess) return attr;
+    const int64_t blocks = (int64_t)bp.f.rows * bp.f.nc * bp.f.H;
+    if (blocks == 0) return hipSuccess;
+    hipLaunchKernelGGL(kern, dim3((unsigned)blocks), dim3(256), lds, stream, bp);
+    return hipGetLastError();
+}
+
+template <typename IO, int N, int PB>
 hipError_t launch_delta_grad(const DeltaBwdParams& bp, hipStream_t stream)
 {
     auto* const kern = &delta_grad_kernel<IO, N, PB>;
@@ -766,13 +842,15 @@ template <typename IO, int N>
 hipError_t bwd_n(const DeltaBwdParams& bp, hipStream_t stream)
 {
     const DeltaParams& p = bp.f;
-    hipError_t e = launch_delta_chunks<IO, N, true>(p, bp.ttf, bp.atf, stream);
+    hipError_t e = launch_delta_chunks<IO, N, true>(p, stream);
     if (e != hipSuccess) return e;
-    const int64_t blocks = (int64_t)p.rows * p.nc * p.H;
-    if (blocks > 0) {
-        hipLaunchKernelGGL((delta_pre_kernel<IO, N>), dim3((unsigned)blocks), dim3(256), 0, stream, bp);
-        if ((e = hipGetLastError()) != hipSuccess) return e;
+    switch (p.P) {
+    case 32: e = launch_delta_pre<IO, N, 1>(bp, stream); break;
+    case 64: e = launch_delta_pre<IO, N, 2>(bp, stream); break;
+    case 96: e = launch_delta_pre<IO, N, 3>(bp, stream); break;
+    default: e = launch_delta_pre<IO, N, 4>(bp, stream);
     }
+    if (e != hipSuccess) return e;
     if (p.rows > 0) {
         using Cf = WalkCfg<IO, N, true>;
         auto* const walks = &delta_walks_kernel<IO, N>;
@@ -799,8 +877,8 @@ hipError_t bwd_n(const DeltaBwdParams& bp, hipStream_t stream)
     }
     if (p.G != p.H && tokens > 0) {
         const int64_t n = (tokens * p.G * p.N / 4 + 255) / 256;
-        hipLaunchKernelGGL(delta_heads_kernel, dim3((unsigned)n), dim3(256), 0, stream, bp.dqe, bp.dq, tokens, p.H, p.G, p.N);
-        hipLaunchKernelGGL(delta_heads_kernel, dim3((unsigned)n), dim3(256), 0, stream, bp.dke, bp.dk, tokens, p.H, p.G, p.N);
+        hipLaunchKernelGGL(delta_heads_kernel, dim3((unsigned)n, 2), dim3(256), 0, stream, bp.dqe, bp.dke, bp.dq, bp.dk, tokens,
+                           p.H, p.G, p.N);
         e = hipGetLastError();
     }
     return e;

@@ -42,56 +42,37 @@ __device__ __forceinline__ double wave_inclusive_sum_d(double v)
     return v;
 }
 
-// 16 x 32 operand block (w, kb) of a triangular matrix in LDS as planes: rows
-// tile_row(w, l), columns 32 kb + 8 g ..+7 (TR: of its transpose), zero outside
-// the triangle.
-template <int PL, int LD, bool TR>
-__device__ __forceinline__ void put_block(bf16* dst, const float* M, int w, int kb, int l, int g, int lane)
-{
-    const int row = tile_row(w, l), c0 = 32 * kb;
-    float x[8];
-    if constexpr (TR) {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) x[e] = M[(c0 + 8 * g + e) * LD + row];
-    } else {
-        const f32x4 a = *reinterpret_cast<const f32x4*>(M + row * LD + c0 + 8 * g);
-        const f32x4 b = *reinterpret_cast<const f32x4*>(M + row * LD + c0 + 8 * g + 4);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) { x[e] = a[e]; x[4 + e] = b[e]; }
-    }
-    bf16x8 o[PL];
-#pragma unroll
-    for (int e = 0; e < 8; e += 2) {
-        const int col = c0 + 8 * g + e;
-        const float x0 = (TR ? col >= row : col <= row) ? x[e] : 0.f;
-        const float x1 = (TR ? col + 1 >= row : col + 1 <= row) ? x[e + 1] : 0.f;
-        bf16x2 t[PL];
-        to_planes2<PL>(x0, x1, t);
-#pragma unroll
-        for (int i = 0; i < PL; ++i) { o[i][e] = t[i][0]; o[i][e + 1] = t[i][1]; }
-    }
-#pragma unroll
-    for (int i = 0; i < PL; ++i) *reinterpret_cast<bf16x8*>(dst + i * 512 + lane * 8) = o[i];
-}
+// The operand blocks of a lower triangular matrix in LDS as planes: block (w,
+// kb) has rows tile_row(w, l), columns 32 kb + 8 g ..+7; zero above the diagonal.
 template <int PL, int LD> __device__ __forceinline__ void put_lower(bf16* dst, const float* M, int l, int g, int lane)
 {
 #pragma unroll
     for (int w = 0; w < 4; ++w)
 #pragma unroll
-        for (int kb = 0; kb <= w / 2; ++kb) put_block<PL, LD, false>(dst + low_block(w, kb) * PL * 512, M, w, kb, l, g, lane);
-}
-template <int PL, int LD> __device__ __forceinline__ void put_upper(bf16* dst, const float* M, int l, int g, int lane)
-{
+        for (int kb = 0; kb <= w / 2; ++kb) {
+            const int row = tile_row(w, l), c0 = 32 * kb + 8 * g;
+            const f32x4 a = *reinterpret_cast<const f32x4*>(M + row * LD + c0);
+            const f32x4 b = *reinterpret_cast<const f32x4*>(M + row * LD + c0 + 4);
+            bf16x8 o[PL];
 #pragma unroll
-    for (int w = 0; w < 4; ++w)
+            for (int e = 0; e < 8; e += 2) {
+                const float x = e < 4 ? a[e & 3] : b[e & 3], y = e < 4 ? a[(e & 3) + 1] : b[(e & 3) + 1];
+                bf16x2 t[PL];
+                to_planes2<PL>(c0 + e <= row ? x : 0.f, c0 + e + 1 <= row ? y : 0.f, t);
 #pragma unroll
-        for (int kb = w / 2; kb < 2; ++kb) put_block<PL, LD, true>(dst + up_block(w, kb) * PL * 512, M, w, kb, l, g, lane);
+                for (int i = 0; i < PL; ++i) { o[i][e] = t[i][0]; o[i][e + 1] = t[i][1]; }
+            }
+#pragma unroll
+            for (int i = 0; i < PL; ++i)
+                *reinterpret_cast<bf16x8*>(dst + (low_block(w, kb) * PL + i) * 512 + lane * 8) = o[i];
+        }
 }
 
 // What one chunk of one head needs besides its rows:
 //   T = (I + M)^-1, A = scale D o Q K^T (rows divided by their norms where the
 //   call asks for it), and per token  beta | beta e^G / |k| | e^(G_last - G) /
-//   |k| | scale e^G / |q|, then e^G_last.
+//   |k| | scale e^G / |q| | e^G_last.
+// BWD: without A and the last but one, with 1 / |k| | G's two parts instead.
 // One wavefront per chunk and head, on its own: no barriers, and the steps
 // that wait on each other (the sums over the chunk, the inverse) run beside
 // those of the other wavefronts on the SIMD.  K and Q rows are the operands as
@@ -107,10 +88,9 @@ template <int PL, int LD> __device__ __forceinline__ void put_upper(bf16* dst, c
 // zero.  Rows past the end read the last row again; their beta is 0 and their
 // g is 0, which makes their rows of T the identity's.
 template <typename IO, int N, bool BWD>
-__global__ __launch_bounds__(64, 2) void delta_chunk_kernel(const DeltaParams p, bf16* ttf, bf16* atf)
+__global__ __launch_bounds__(64, 2) void delta_chunk_kernel(const DeltaParams p)
 {
     constexpr int KP = DeltaPlanes<IO>::io, WP = DeltaPlanes<IO>::wide, OP = DeltaPlanes<IO>::out;
-    constexpr int AP = BWD ? WP : OP;     // the gradient's path is float32 throughout
     constexpr int KB = N / 32, LD = 68;
     __shared__ __attribute__((aligned(16))) float sM[64 * LD];
     __shared__ __attribute__((aligned(16))) float sGh[64], sGl[64], sBk[64], sRk[64], sRq[64];
@@ -145,7 +125,7 @@ __global__ __launch_bounds__(64, 2) void delta_chunk_kernel(const DeltaParams p,
     // the larger rows would not fit beside K's: they are read tile by tile
     constexpr bool ALLQ = KP == 1 && N < 128;
 #pragma unroll
-    for (int rt = 0; rt < (ALLQ ? 4 : 1); ++rt)
+    for (int rt = 0; rt < (BWD ? 0 : ALLQ ? 4 : 1); ++rt)
 #pragma unroll
         for (int kb = 0; kb < KB; ++kb) qr[rt][kb].load(qp + off[rt] + 32 * kb, true);
 
@@ -178,7 +158,7 @@ __global__ __launch_bounds__(64, 2) void delta_chunk_kernel(const DeltaParams p,
                 mma_planes<KP, KP, WP>(a, j, kk[rt][ct]);
             }
         }
-    float rk = 1.f, rq = 1.f;
+    float rk = 1.f;
     if (p.l2norm) {   // |k|^2 is the diagonal
 #pragma unroll
         for (int rt = 0; rt < 4; ++rt)
@@ -204,37 +184,39 @@ __global__ __launch_bounds__(64, 2) void delta_chunk_kernel(const DeltaParams p,
     }
 #pragma unroll
     for (int rt = 0; rt < 4; ++rt) {
-        f32x4 qk[4] = {fz, fz, fz, fz};
-        float q2 = 0.f;
+        f32x4 qk[4] = {fz, fz, fz, fz}, rq4 = fz;
+        if constexpr (!BWD) {
+            float q2 = 0.f;
 #pragma unroll
-        for (int kb = 0; kb < KB; ++kb) {
-            bf16x8 a[KP];
-            qr[ALLQ ? rt : 0][kb].planes(a);
-            if (p.l2norm)
+            for (int kb = 0; kb < KB; ++kb) {
+                bf16x8 a[KP];
+                qr[ALLQ ? rt : 0][kb].planes(a);
+                if (p.l2norm)
 #pragma unroll
-                for (int e = 0; e < 8; ++e) q2 += qr[ALLQ ? rt : 0][kb].get(e) * qr[ALLQ ? rt : 0][kb].get(e);
+                    for (int e = 0; e < 8; ++e) q2 += qr[ALLQ ? rt : 0][kb].get(e) * qr[ALLQ ? rt : 0][kb].get(e);
 #pragma unroll
-            for (int ct = 0; ct <= rt; ++ct) {
-                bf16x8 j[KP];
-                kr[ct][kb].planes(j);
-                mma_planes<KP, KP, WP>(a, j, qk[ct]);
+                for (int ct = 0; ct <= rt; ++ct) {
+                    bf16x8 j[KP];
+                    kr[ct][kb].planes(j);
+                    mma_planes<KP, KP, WP>(a, j, qk[ct]);
+                }
+                if (!ALLQ && rt < 3) qr[0][kb].load(qp + off[rt < 3 ? rt + 1 : 3] + 32 * kb, true);
             }
-            if (!ALLQ && rt < 3) qr[0][kb].load(qp + off[rt < 3 ? rt + 1 : 3] + 32 * kb, true);
+            if (p.l2norm) {
+                q2 += __shfl_xor(q2, 16);
+                q2 += __shfl_xor(q2, 32);
+                q2 = __builtin_amdgcn_rsqf(q2 + p.eps);
+            } else {
+                q2 = 1.f;
+            }
+            if (g == 0) sRq[16 * rt + l] = q2;
+            wave_order();
+            rq4 = *reinterpret_cast<const f32x4*>(&sRq[16 * rt + 4 * g]);
+#pragma unroll
+            for (int r = 0; r < 4; ++r) rq4[r] *= p.scale;
         }
-        if (p.l2norm) {
-            q2 += __shfl_xor(q2, 16);
-            q2 += __shfl_xor(q2, 32);
-            q2 = __builtin_amdgcn_rsqf(q2 + p.eps);
-        } else {
-            q2 = 1.f;
-        }
-        if (g == 0) sRq[16 * rt + l] = q2;
-        wave_order();
         const f32x4 gh4 = *reinterpret_cast<const f32x4*>(&sGh[16 * rt + 4 * g]);
         const f32x4 gl4 = *reinterpret_cast<const f32x4*>(&sGl[16 * rt + 4 * g]);
-        f32x4 rq4 = *reinterpret_cast<const f32x4*>(&sRq[16 * rt + 4 * g]);
-#pragma unroll
-        for (int r = 0; r < 4; ++r) rq4[r] *= p.scale;
         const f32x4 bk4 = *reinterpret_cast<const f32x4*>(&sBk[16 * rt + 4 * g]);
 #pragma unroll
         for (int ct = 0; ct <= rt; ++ct)
@@ -244,30 +226,27 @@ __global__ __launch_bounds__(64, 2) void delta_chunk_kernel(const DeltaParams p,
                 const int i = 4 * g + r;   // row in the tile
                 float D = __builtin_amdgcn_exp2f((gh4[r] - cgh[ct]) + (gl4[r] - cgl[ct])) * crk[ct];
                 if (diag && l > i) D = 0.f;
-                sM[(16 * rt + i) * LD + 16 * ct + l] = rq4[r] * D * qk[ct][r];
+                if constexpr (!BWD) sM[(16 * rt + i) * LD + 16 * ct + l] = rq4[r] * D * qk[ct][r];
                 // D's last use is M: kk becomes M here
                 kk[rt][ct][r] = (diag && l >= i) ? 0.f : bk4[r] * D * kk[rt][ct][r];
             }
     }
-    wave_order();
-    rq = sRq[lane];
     {
-        float* sc = p.sc + ci * (kDScal * 64);
-        sc[lane] = bv;
-        sc[64 + lane] = bv * eG * rk;
-        sc[128 + lane] = dG * rk;
-        sc[192 + lane] = p.scale * eG * rq;
-        sc[256 + lane] = __builtin_amdgcn_exp2f((float)Gl);   // e^G_last, for every lane
-        if (BWD) {
-            sc[320 + lane] = rk;
-            sc[384 + lane] = gh;
-            sc[448 + lane] = sGl[lane];
+        float* sc = p.sc + ci * (kDScal * 64) + lane;
+        sc[0] = bv;
+        sc[64] = bv * eG * rk;
+        sc[128] = dG * rk;
+        sc[256] = __builtin_amdgcn_exp2f((float)Gl);   // e^G_last, for every lane
+        if constexpr (BWD) {
+            sc[320] = rk;
+            sc[384] = gh;
+            sc[448] = sGl[lane];
+        } else {
+            wave_order();
+            sc[192] = p.scale * eG * sRq[lane];
+            put_lower<OP, LD>(p.af + ci * (kTriBlocks * OP * 512), sM, l, g, lane);
         }
     }
-    if (!BWD)
-        put_lower<AP, LD>(p.af + ci * (kTriBlocks * AP * 512), sM, l, g, lane);
-    else
-        put_upper<AP, LD>(atf + ci * (kTriBlocks * AP * 512), sM, l, g, lane);
 
     // M takes A's place
     wave_order();
@@ -345,15 +324,14 @@ __global__ __launch_bounds__(64, 2) void delta_chunk_kernel(const DeltaParams p,
     }
     wave_order();
     put_lower<WP, LD>(p.tf + ci * (kTriBlocks * WP * 512), sM, l, g, lane);
-    if (BWD) put_upper<WP, LD>(ttf + ci * (kTriBlocks * WP * 512), sM, l, g, lane);
 }
 
 template <typename IO, int N, bool BWD>
-hipError_t launch_delta_chunks(const DeltaParams& p, bf16* ttf, bf16* atf, hipStream_t stream)
+hipError_t launch_delta_chunks(const DeltaParams& p, hipStream_t stream)
 {
     const int64_t blocks = (int64_t)p.rows * p.nc * p.H;
     if (blocks == 0) return hipSuccess;
-    hipLaunchKernelGGL((delta_chunk_kernel<IO, N, BWD>), dim3((unsigned)blocks), dim3(64), 0, stream, p, ttf, atf);
+    hipLaunchKernelGGL((delta_chunk_kernel<IO, N, BWD>), dim3((unsigned)blocks), dim3(64), 0, stream, p);
     return hipGetLastError();
 }
 

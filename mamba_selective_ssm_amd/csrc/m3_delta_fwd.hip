@@ -9,7 +9,7 @@ namespace {
 template <typename IO, int N>
 hipError_t fwd_n(const DeltaParams& p, hipStream_t stream)
 {
-    const hipError_t e = launch_delta_chunks<IO, N, false>(p, nullptr, nullptr, stream);
+    const hipError_t e = launch_delta_chunks<IO, N, false>(p, stream);
     if (e != hipSuccess) return e;
     if constexpr (sizeof(IO) == 2) {
         if ((int64_t)p.rows * p.H * (p.P / 16) > 256) {
