@@ -441,6 +441,8 @@ int m3_decode_supported(int64_t dstate, int64_t headdim, int64_t rank, int32_t i
  * three bf16 values and float32 sums: states and gradients have float32's
  * accuracy for both io dtypes.  NaN and Inf inputs propagate as in
  * m3_scan_fwd (within their chunk of 64 tokens also to earlier tokens).
+ * A workspace holds one call's intermediate values: calls that may run beside
+ * each other (streams, replayed graphs) need one each.
  */
 typedef struct {
     int64_t batch, seqlen, nheads, ngroups, headdim, dstate;

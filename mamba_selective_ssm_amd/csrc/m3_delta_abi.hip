@@ -27,9 +27,9 @@ bool on4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 size_t up256(size_t v) { return (v + 255) / 256 * 256; }
 m3_status status_of(hipError_t e) { return static_cast<m3_status>(m3::record_hip(e)); }
 
-// HIP launches count their threads in 32 bits; all kernels here have 256 or
-// more to a workgroup.
-constexpr int64_t kMaxBlocks256 = (int64_t)1 << 24;
+// HIP launches count a dimension's threads in 32 bits.
+constexpr int64_t kMaxThreads = ((int64_t)1 << 32) - 1;
+constexpr int64_t kMaxBlocks256 = kMaxThreads / 256;
 
 // Sizes shared by the three calls.
 m3_status check_sizes(int64_t batch, int64_t seqlen, int64_t H, int64_t G, int64_t P, int64_t N, int32_t io, int32_t l2norm,
@@ -55,7 +55,7 @@ struct DeltaPlan {
     size_t fwd, bwd;           // whole workspaces
 };
 
-m3_status plan_delta(const m3_delta_args* a, DeltaPlan* out)
+m3_status plan_delta(const m3_delta_args* a, bool train, DeltaPlan* out)
 {
     if (a == nullptr) return M3_ERR_NULL;
     const m3_status s = check_sizes(a->batch, a->seqlen, a->nheads, a->ngroups, a->headdim, a->dstate, a->io_dtype,
@@ -64,10 +64,19 @@ m3_status plan_delta(const m3_delta_args* a, DeltaPlan* out)
     const bool packed = a->cu_seqlens != nullptr;
     if (packed && (a->max_seqlen < 0 || a->max_seqlen > a->seqlen)) return M3_ERR_OPTION;
     const int64_t longest = packed ? a->max_seqlen : a->seqlen, H = a->nheads;
-    if (longest > ((int64_t)1 << 30)) return M3_ERR_UNSUPPORTED;
+    if (longest > ((int64_t)1 << 30) || a->seqlen > ((int64_t)1 << 38)) return M3_ERR_UNSUPPORTED;
     out->G = a->ngroups > 0 ? a->ngroups : H;
     out->nc = (longest + m3::kDC - 1) / m3::kDC;
     if (a->batch > 0 && H > 0 && out->nc > kMaxBlocks256 / (a->batch * H)) return M3_ERR_UNSUPPORTED;
+    // the walks: 16 columns of one row and head to a workgroup, 448 threads, or
+    // twice 320; the other kernels that the gradient adds
+    const int64_t slices = (a->batch * H + 7) / 8 * 8 * (a->headdim / 16);
+    if (slices > kMaxThreads / (train ? 640 : 448)) return M3_ERR_UNSUPPORTED;
+    if (train) {
+        const int64_t tok = packed ? a->seqlen : a->batch * a->seqlen;   // dense: 64 chunks' worth at most
+        if (a->batch >= kMaxBlocks256) return M3_ERR_UNSUPPORTED;
+        if (H > 0 && tok > 4 * (kMaxThreads - 255) / (out->G * a->dstate)) return M3_ERR_UNSUPPORTED;
+    }
     const int64_t slots = packed ? a->seqlen / m3::kDC + a->batch + 1 : a->batch * out->nc;
     out->chunks = slots * H;
     const int wide = 3, opl = a->io_dtype == M3_F32 ? 3 : 2;
@@ -130,7 +139,7 @@ m3_status check_pool(const m3_pool& p)
     if (p.slots > ((int64_t)1 << 30)) return M3_ERR_UNSUPPORTED;
     for (int i = 0; i < p.narrays; ++i) {
         if (p.row_bytes[i] < 1) return M3_ERR_SHAPE;
-        if (p.row_bytes[i] > ((int64_t)1 << 33)) return M3_ERR_UNSUPPORTED;
+        if (p.row_bytes[i] > ((int64_t)1 << 33) || p.slots * (p.row_bytes[i] >> 16) > ((int64_t)1 << 30)) return M3_ERR_UNSUPPORTED;
         if (p.slots > 0 && p.data[i] == nullptr) return M3_ERR_NULL;
         if (!on16(p.data[i])) return M3_ERR_ALIGN;
     }
@@ -210,19 +219,19 @@ int m3_delta_supported(int64_t dstate, int64_t headdim, int32_t io_dtype)
 size_t m3_delta_workspace_bytes(const m3_delta_args* a)
 {
     DeltaPlan pl;
-    return plan_delta(a, &pl) == M3_OK ? pl.fwd : 0;
+    return plan_delta(a, false, &pl) == M3_OK ? pl.fwd : 0;
 }
 
 size_t m3_delta_bwd_workspace_bytes(const m3_delta_bwd_args* a)
 {
     DeltaPlan pl;
-    return a != nullptr && plan_delta(&a->in, &pl) == M3_OK ? pl.bwd : 0;
+    return a != nullptr && plan_delta(&a->in, true, &pl) == M3_OK ? pl.bwd : 0;
 }
 
 m3_status m3_delta_fwd(const m3_delta_args* a, void* stream)
 {
     DeltaPlan pl;
-    const m3_status s = plan_delta(a, &pl);
+    const m3_status s = plan_delta(a, false, &pl);
     if (s != M3_OK) return s;
     if (a->slots != nullptr && (a->nslots < 0 || a->nslots > ((int64_t)1 << 30))) return M3_ERR_OPTION;
     if (a->batch * a->nheads == 0) return M3_OK;
@@ -259,6 +268,8 @@ m3_status m3_delta_step(const m3_delta_step_args* a, void* stream)
     const m3_status s = check_sizes(a->batch, 1, a->nheads, a->ngroups, a->headdim, a->dstate, a->io_dtype, a->l2norm,
                                     a->scale, a->norm_eps);
     if (s != M3_OK) return s;
+    // a wavefront to 32 columns of one row and head, four to a workgroup
+    if (a->batch * a->nheads * (a->headdim / 32) > (kMaxThreads - 255) / 64) return M3_ERR_UNSUPPORTED;
     if (a->slots != nullptr && (a->nslots < 0 || a->nslots > ((int64_t)1 << 30))) return M3_ERR_OPTION;
     if (a->batch * a->nheads == 0) return M3_OK;
     if (!a->q || !a->k || !a->v || !a->g || !a->beta || !a->h || !a->o) return M3_ERR_NULL;
@@ -292,7 +303,7 @@ m3_status m3_delta_bwd(const m3_delta_bwd_args* b, void* stream)
     if (b == nullptr) return M3_ERR_NULL;
     const m3_delta_args* a = &b->in;
     DeltaPlan pl;
-    const m3_status s = plan_delta(a, &pl);
+    const m3_status s = plan_delta(a, true, &pl);
     if (s != M3_OK) return s;
     if (a->slots != nullptr || a->h_out != nullptr || a->o != nullptr) return M3_ERR_UNSUPPORTED;
     const DeltaBytes n = bytes_of(a, pl);
@@ -417,7 +428,7 @@ m3_status m3_pool_compact(const m3_pool_compact_args* a, void* stream)
 m3_status m3_pool_free(int32_t* live, int64_t slots, const int32_t* list, int64_t count, void* stream)
 {
     if (slots < 0 || count < 0) return M3_ERR_SHAPE;
-    if (count > ((int64_t)1 << 31) || slots > ((int64_t)1 << 30)) return M3_ERR_UNSUPPORTED;
+    if (count > kMaxThreads - 255 || slots > ((int64_t)1 << 30)) return M3_ERR_UNSUPPORTED;
     if (slots == 0 || count == 0) return M3_OK;
     if (live == nullptr || list == nullptr) return M3_ERR_NULL;
     if (!on4(live) || !on4(list)) return M3_ERR_ALIGN;

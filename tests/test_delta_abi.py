@@ -248,3 +248,42 @@ def test_binding_refusals():
         m3_pool_copy((), (), torch.zeros(1, dtype=torch.int32), torch.zeros(1, dtype=torch.int32))
     with pytest.raises(ValueError):
         m3_pool_free(torch.zeros(4, dtype=torch.int32), torch.zeros(1, dtype=torch.int32))
+
+
+LAUNCH = [   # launches count their threads in 32 bits: the first size that does not fit, and the last that does
+    ("fwd", dict(nheads=1 << 10, ngroups=0, headdim=128), "batch", (((1 << 32) - 1) // 448 // 8) // (1 << 10) + 1),
+    ("bwd", dict(nheads=1 << 10, ngroups=0, headdim=128), "batch", (((1 << 32) - 1) // 640 // 8) // (1 << 10) + 1),
+    ("bwd", dict(nheads=1, ngroups=0, dstate=32, cu_seqlens=at(9), max_seqlen=64), "seqlen", (1 << 29) - 31),
+    ("fwd", dict(cu_seqlens=at(9), max_seqlen=64), "seqlen", (1 << 38) + 1),
+]
+
+
+@pytest.mark.parametrize("what,kw,name,first", LAUNCH)
+def test_sizes_beyond_a_launch(lib, what, kw, name, first):
+    def need(n):
+        a = fwd_args(**{**kw, name: n})
+        if what == "fwd":
+            return lib.m3_delta_workspace_bytes(ctypes.byref(a)), lib.m3_delta_fwd(ctypes.byref(a), None)
+        b = delta.DeltaBwdArgs()
+        a.o = a.h_out = None
+        b.in_ = a
+        return lib.m3_delta_bwd_workspace_bytes(ctypes.byref(b)), lib.m3_delta_bwd(ctypes.byref(b), None)
+
+    assert need(first) == (0, -3)
+    b, st = need(first - 1)
+    assert b > 0 and st != -3
+
+
+def test_step_beyond_a_launch(lib):
+    a = delta.DeltaStepArgs(batch=1 << 12, nheads=1 << 12, headdim=128, dstate=32, io_dtype=1, scale=1.0)
+    assert lib.m3_delta_step(ctypes.byref(a), None) == -3
+    a.batch -= 1
+    assert lib.m3_delta_step(ctypes.byref(a), None) == -1   # fits: its null pointers are next
+
+
+def test_pools_beyond_address_arithmetic(lib):
+    """slots x row bytes of one array is bounded, so that no product of the checks wraps."""
+    d = desc(0, slots=1 << 30, rows=(1 << 33, 512))
+    a = copy_args(src=d, dst=desc(2, slots=1 << 30, rows=(1 << 33, 512)))
+    assert lib.m3_pool_copy(ctypes.byref(a), None) == -3
+    assert lib.m3_pool_free(at(0), 4, at(8), (1 << 32) - 255, None) == -3
