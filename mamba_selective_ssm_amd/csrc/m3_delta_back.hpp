@@ -34,7 +34,9 @@ __device__ __forceinline__ float groups_sum(float v)
 // workgroup per chunk and head: wave w takes tokens 16 w .. + 15 of E1 and rows
 // 16 w .. (and 16 w + 64 ..) of E2, all columns.  A comes out of Q K^T as the
 // second operand.  Bound by memory: it reads a chunk's K, Q and dO and writes
-// 4 (64 + N) P bytes.
+// 4 (64 + N) P bytes: 56 KB a chunk and head at N = P = 64, 31 us for 2048 of
+// them (3.8 TB/s).  A read from the chunk kernel instead of made here cost 12 KB
+// of writes and reads each: the whole gradient took 245 for 215 us.
 template <typename IO, int N, int PB> struct PreCfg {
     static constexpr int KP = DeltaPlanes<IO>::io, LQ = N + 8, LO = 32 * PB + 8;
     static constexpr int q = KP * 64 * LQ * 2, o = 2 * q, f = o + KP * 64 * LO * 2, total = f + 4 * 64 * 4;
@@ -384,7 +386,9 @@ __device__ __forceinline__ void delta_back(const DeltaBwdParams& bp, int64_t bid
 
 // Both walks of the gradient: neither needs the other, and each alone waits
 // for its own chain most of the time.  All workgroups of one, then of the
-// other, so that a CU gets one of each.
+// other, so that a CU gets one of each.  78 us at 256 slices, 32 chunks, N = P =
+// 64 (107 as two launches), about 156 KB of memory traffic a chunk and head
+// (4.1 TB/s).
 template <typename IO, int N>
 __global__ __launch_bounds__(320) void delta_walks_kernel(const DeltaBwdParams bp)
 {
@@ -410,8 +414,11 @@ template <typename IO, int N, int PB> struct GradCfg {
 // neighbours.  The rows of dO, dR and U are second operands as they lie in
 // memory; S0 and dS1 go through LDS in tiles of 16 rows, split once for all
 // four waves, the next tile's loads in flight; then U takes that place, then
-// B1 and B2, whose columns dk needs.  About 250 products of 16x16x32 and as
-// many bytes as a chunk's two states and its rows, read once.
+// B1 and B2, whose columns dk needs.  Bound by memory: a chunk's two states, U,
+// dR and its rows come in once, 64 KB of gradients go out; 144 KB a chunk and
+// head at N = P = 64, 90 us for 2048 of them (3.3 TB/s) with two workgroups to a
+// CU.  With a lane for four rows instead of one (products not transposed) the
+// factors, sums and stores were four times as many: 193 us.
 template <typename IO, int N, int PB>
 __global__ __launch_bounds__(256, PB <= 2 ? 2 : 1) void delta_grad_kernel(const DeltaBwdParams bp)
 {
@@ -816,7 +823,8 @@ hipError_t launch_delta_pre(const DeltaBwdParams& bp, hipStream_t stream)
     auto* const kern = &delta_pre_kernel<IO, N, PB>;
     constexpr size_t lds = PreCfg<IO, N, PB>::total;
     static_assert(lds <= 160 * 1024, "a workgroup's LDS");
-    static const hipError_t attr = delta_allow_lds(kern, lds);
+    static std::atomic<uint64_t> done{0};
+    const hipError_t attr = delta_allow_lds(kern, lds, done);
     if (attr != hipSuccess) return attr;
     const int64_t blocks = (int64_t)bp.f.rows * bp.f.nc * bp.f.H;
     if (blocks == 0) return hipSuccess;
@@ -830,7 +838,8 @@ hipError_t launch_delta_grad(const DeltaBwdParams& bp, hipStream_t stream)
     auto* const kern = &delta_grad_kernel<IO, N, PB>;
     constexpr size_t lds = GradCfg<IO, N, PB>::total;
     static_assert(lds <= 160 * 1024, "a workgroup's LDS");
-    static const hipError_t attr = delta_allow_lds(kern, lds);
+    static std::atomic<uint64_t> done{0};
+    const hipError_t attr = delta_allow_lds(kern, lds, done);
     if (attr != hipSuccess) return attr;
     const int64_t blocks = (int64_t)bp.f.rows * bp.f.nc * bp.f.H;
     if (blocks == 0) return hipSuccess;
@@ -855,8 +864,8 @@ hipError_t bwd_n(const DeltaBwdParams& bp, hipStream_t stream)
         using Cf = WalkCfg<IO, N, true>;
         auto* const walks = &delta_walks_kernel<IO, N>;
         static_assert(Cf::total <= 160 * 1024, "a workgroup's LDS");
-        static const hipError_t attr = delta_allow_lds(walks, Cf::total);
-        if (attr != hipSuccess) return attr;
+        static std::atomic<uint64_t> done{0};
+        if ((e = delta_allow_lds(walks, Cf::total, done)) != hipSuccess) return e;
         const int64_t n = ((int64_t)p.rows * p.H + 7) / 8 * 8 * (p.P / 16);
         const size_t lds = Cf::total;
         hipLaunchKernelGGL(walks, dim3((unsigned)(2 * n)), dim3(64 * Cf::waves), lds, stream, bp);

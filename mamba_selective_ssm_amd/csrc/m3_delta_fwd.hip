@@ -6,6 +6,17 @@ namespace m3 {
 
 namespace {
 
+// Which walk.  A slice is 16 columns of one row and head.  Up to one slice per
+// CU its chain of products is the call's time, and four wavefronts on one slice
+// (delta_walk) take less than one wavefront's registers (delta_wide): 39 against
+// 53 us at 256 slices, 2048 tokens, N = 64.  With more, a CU's LDS reads are,
+// and delta_wide has a quarter of them (whole calls over 2048 tokens, us, P =
+// 64, delta_walk / delta_wide): N = 64: 288 slices 104 / 100, 384: 112 / 107,
+// 512: 128 / 122, 544: 170 / 128, 768: 264 / 190, 1024: 337 / 237; N = 32, 512:
+// 113 / 97; N = 128, 288: 130 / 122, 512: 183 / 151, 1024: 368 / 312.  Where P
+// and the LDS allow, 64 columns go to a workgroup: with 32 of them the calls
+// above 512 slices are two rounds over the chip (N = 64: 544: 185, 768: 245,
+// 1024: 281 us), those up to 512 take the same time.
 template <typename IO, int N>
 hipError_t fwd_n(const DeltaParams& p, hipStream_t stream)
 {

@@ -11,6 +11,9 @@
 // rg N/8 .. +N/8-1 of columns 4 cq .. +3, so its k and q values are contiguous
 // too.  All its loads are in flight at once (N/8 of 16 bytes a lane), and the
 // only exchange is the sum over the eight row groups.
+// 256 rows x 32 heads, N = 128, P = 64: 537 MB of state in 96 us, 5.6 TB/s (a
+// copy of 4 GiB runs at 4.7).  Loads that bypass the caches took 108 us, one or
+// two wavefronts to a workgroup instead of four 102 and 98.
 #include "m3_delta.hpp"
 
 namespace m3 {

@@ -1,6 +1,7 @@
 // Gated delta rule: the walk over a row's chunks.
 #pragma once
 
+#include <atomic>
 #include <type_traits>
 
 #include "m3_delta.hpp"
@@ -17,25 +18,37 @@ namespace m3 {
 //     of each product; a result leaves as planes in operand order (tile_row),
 //     so that all four read it back with plain 16-byte reads after a barrier;
 //   - a loader wavefront moves K, T, V and the factors from memory straight to
-//     LDS, NBUF - 1 chunks ahead;
+//     LDS, NBUF - 1 chunks ahead (float32 K through its registers, where it is
+//     split into planes: read two chunks ahead, 29 us for 37 at 32 slices of 13
+//     chunks, N = 64);
 //   - two output wavefronts make O from the S and U planes, Q S
 //     while the state goes through T, A U during the next chunk's first stage.
+// Three buffers (two chunks ahead) for the forward bf16 walk: with two the 256
+// slices below take 5 us more, N = 128 over 65536 tokens 2098 -> 2503 us.
+//
+// A chunk takes about 2300 cycles at N = 64, LDS busy for 1090 of them and
+// waiting on bank conflicts for 310; 3170, 1470 and 460 at N = 128.  Over 32
+// chunks, 256 slices: 39 us (N = 64); over 1024 chunks, 128 slices at N = 128:
+// 1660 us.  The first kernel, one workgroup of four wavefronts that loaded
+// and computed in turn, took 110 and 4730 us.
 //
 // K rows lie in LDS in blocks of 8 values whose place is permuted by the row
 // (k_block), which keeps both the row-wise and the transposed reads free of
 // bank conflicts without padding, as the direct loads need it.
 // TRAIN (the gradient's two walks, which run beside each other): no output
 // wavefronts, and buffers for one chunk ahead only, so that two workgroups fit
-// on a CU.
+// on a CU: 90 us for both walks at 256 slices each (N = P = 64, 32 chunks), 102
+// to 113 us with two chunks ahead and one workgroup to a CU.
 template <typename IO, int N, bool TRAIN> struct WalkCfg {
     static constexpr int KP = DeltaPlanes<IO>::io, WP = DeltaPlanes<IO>::wide, OP = DeltaPlanes<IO>::out;
     static constexpr bool DIRECT = KP == 1;           // io values are operands as they are: loads go straight to LDS
     static constexpr int NBUF = DIRECT && !TRAIN ? 3 : 2;
     static constexpr int KB = N / 32, NT = N / 16, TI = (NT + 3) / 4;
     static constexpr int outs = TRAIN ? 0 : 2, waves = 4 + outs + 1;
-    // bytes of one buffer (T apart: those with one chunk ahead have one T)
+    // bytes of one buffer (T apart: the gradient has one, and float32 at N = 128,
+    // whose planes leave room for one)
     static constexpr int k = 0, f = k + KP * 64 * N * 2, v = f + 5 * 256, buf = v + (DIRECT ? 64 * 32 : 0);
-    static constexpr int tsize = kTriBlocks * WP * 1024, TB = DIRECT && !TRAIN ? NBUF : 1;
+    static constexpr int tsize = kTriBlocks * WP * 1024, TB = TRAIN || (!DIRECT && N == 128) ? 1 : NBUF;
     static constexpr int t = NBUF * buf;
     // then the planes of S, R, d U, U, and the rows of O
     static constexpr int ex = t + TB * tsize, s = 0, r = s + WP * KB * 1024, u2 = r + WP * 2048, u = u2 + WP * 2048,
@@ -69,6 +82,11 @@ template <int n> __device__ __forceinline__ void wait_loads()
 {
     __builtin_amdgcn_s_waitcnt((n & 15) | ((n >> 4) << 14) | (7 << 4) | (15 << 8));
 }
+// And for all of its LDS writes.
+template <int n> __device__ __forceinline__ void wait_loads_lds()
+{
+    __builtin_amdgcn_s_waitcnt((n & 15) | ((n >> 4) << 14) | (7 << 4));
+}
 
 // The loader wavefront of a walk: K, the triangle `tri`, the factors and (not
 // REV) V of each chunk to LDS, NBUF - 1 steps ahead of their use.  REV: chunks
@@ -95,12 +113,39 @@ __device__ __forceinline__ void walk_loader(const DeltaParams& p, char* wlds, co
     };
     // factors, V, K: loads i0..i1-1 of `head`
     constexpr int nk = 64 * N * 2 / 1024, nv = REV ? 0 : 2, head = 2 + nv + nk;
+    constexpr int RPL = 512 / N, NR = 64 / RPL;   // K rows of one load; loads of a chunk's K
+    // float32 K waits in registers, one more chunk ahead, for its split into
+    // planes; `split` also reads the next chunk's row in its place
+    RawRow8<IO> raw[Cf::DIRECT ? 1 : NR];
+    auto fetch = [&](int s, int i) {
+        if constexpr (!Cf::DIRECT) {
+            s = s < nch ? s : nch - 1;
+            const int c = REV ? nch - 1 - s : s;
+            const int end = c == nch - 1 ? nlast - 1 : kDC - 1;
+            const int t = RPL * i + lane / (N / 8), j = k_block<N>(t, lane % (N / 8));
+            raw[i].load(kp + (int64_t)c * kDC * rs + (t < end ? t : end) * rs + 8 * j, true);
+        }
+    };
+    auto split = [&](int s, int i0, int i1) {
+        if constexpr (!Cf::DIRECT) {
+            char* buf = wlds + (s % NBUF) * Cf::buf;
+#pragma unroll
+            for (int i = 0; i < NR; ++i) {
+                if (i < i0 || i >= i1) continue;
+                bf16x8 o[KP];
+                raw[i].planes(o);
+#pragma unroll
+                for (int q = 0; q < KP; ++q)
+                    *reinterpret_cast<bf16x8*>(buf + Cf::k + q * (64 * N * 2) + 1024 * i + 16 * lane) = o[q];
+                fetch(s + 1, i);
+            }
+        }
+    };
     auto stage = [&](int s, int i0, int i1) {
         const int c = REV ? nch - 1 - s : s;
         char* buf = wlds + (s % NBUF) * Cf::buf;
         const int end = c == nch - 1 ? nlast - 1 : kDC - 1;   // last row to read
         const IO* kc = kp + (int64_t)c * kDC * rs;
-        constexpr int RPL = 512 / N;   // K rows of one load
         const float* fsrc = p.sc + (ci0 + (int64_t)c * p.H) * (kDScal * 64);
         if (i0 == 0) {
             to_lds16(buf + Cf::f, fsrc + 4 * lane);
@@ -121,18 +166,6 @@ __device__ __forceinline__ void walk_loader(const DeltaParams& p, char* wlds, co
                     to_lds16(buf + Cf::v + 1024 * i, vc + (t < end ? t : end) * vs + 8 * (lane % 2));
                 }
             }
-        } else {
-#pragma unroll 4
-            for (int i = 0; i < 64 / RPL; ++i) {
-                const int t = RPL * i + lane / (N / 8), j = k_block<N>(t, lane % (N / 8));
-                RawRow8<IO> x;
-                x.load(kc + (t < end ? t : end) * rs + 8 * j, true);
-                bf16x8 o[KP];
-                x.planes(o);
-#pragma unroll
-                for (int q = 0; q < KP; ++q)
-                    *reinterpret_cast<bf16x8*>(buf + Cf::k + q * (64 * N * 2) + 1024 * i + 16 * lane) = o[q];
-            }
         }
     };
     // s_barrier alone: the release of __syncthreads would wait for every load
@@ -141,37 +174,55 @@ __device__ __forceinline__ void walk_loader(const DeltaParams& p, char* wlds, co
         __builtin_amdgcn_s_barrier();
         asm volatile("" ::: "memory");
     };
+    if (!Cf::DIRECT && nch > 0)
+#pragma unroll
+        for (int i = 0; i < NR; ++i) fetch(0, i);
 #pragma unroll
     for (int s = 0; s < NBUF - 1; ++s)
         if (s < nch) {
             stage(s, 0, head);
+            split(s, 0, NR);
             if (s < Cf::TB) stage_t(s, 0, 3 * kTriBlocks);
         }
     asm volatile("" ::: "memory");
     __builtin_amdgcn_s_waitcnt(0);
     barrier();
     for (int s = 0; s < nch; ++s) {
-        // a third of the loads beside each stage: a load takes some 30 cycles
-        // to issue, all of one chunk longer than a stage
+        // a third of the loads (float32: of the splits) beside each stage: a load
+        // takes some 30 cycles to issue, all of one chunk longer than a stage
         constexpr int third = (head + 18) / 3;
         constexpr int k1 = Cf::DIRECT && !T1 && third < head ? third : head, t1 = 2 * third > head ? 2 * third - head : 0;
+        constexpr int NR1 = NR / 3, NR2 = 2 * NR / 3;
         const bool more = s + NBUF - 1 < nch;
-        if (more) stage(s + NBUF - 1, 0, k1);
+        if (more) {
+            stage(s + NBUF - 1, 0, k1);
+            if (!Cf::DIRECT) {
+                if (!T1) stage_t(s + NBUF - 1, 0, 18);
+                asm volatile("" ::: "memory");   // the last loads of a step are rows, for the wait below
+                split(s + NBUF - 1, 0, NR1);
+            }
+        }
         barrier();   // R
-        if (!T1 && more) {
+        if (!Cf::DIRECT && more) split(s + NBUF - 1, NR1, NR2);
+        if (Cf::DIRECT && !T1 && more) {
             if (k1 < head) stage(s + NBUF - 1, k1, head);
             stage_t(s + NBUF - 1, 0, t1);
         }
         barrier();   // U: a single T is free
         if (!T1) {
-            if (more) stage_t(s + NBUF - 1, t1, 18);
+            if (Cf::DIRECT && more) stage_t(s + NBUF - 1, t1, 18);
+            if (!Cf::DIRECT && more) split(s + NBUF - 1, NR2, NR);
         } else if (s + 1 < nch) {
             stage_t(s + 1, 0, 18);
+            asm volatile("" ::: "memory");
+            if (!Cf::DIRECT && more) split(s + NBUF - 1, NR2, NR);
         }
         asm volatile("" ::: "memory");
         // the next chunk has landed
         constexpr int loads = Cf::loads - (REV ? 2 : 0);
         if (NBUF == 3 && more) wait_loads<loads>();
+        else if (!Cf::DIRECT && !T1 && more) wait_loads_lds<2 * NR>();   // (the rows fetched meanwhile)
+        else if (!Cf::DIRECT && more) wait_loads_lds<2 * (NR - NR2)>();
         else __builtin_amdgcn_s_waitcnt(0);
         barrier();   // S
     }
@@ -509,11 +560,18 @@ __global__ __launch_bounds__(64 * 7) void delta_walk_kernel(const DeltaParams p)
     delta_walk<IO, N, false>(p, nullptr, nullptr, blockIdx.x, wlds);
 }
 
-template <typename F> hipError_t delta_allow_lds(F* kern, size_t bytes)
+// Lets `kern` have `bytes` of LDS on the current device, once on each (`done`:
+// a bit per device, one word per kernel).
+template <typename F> hipError_t delta_allow_lds(F* kern, size_t bytes, std::atomic<uint64_t>& done)
 {
-    const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(kern), hipFuncAttributeMaxDynamicSharedMemorySize,
-                                             (int)bytes);
-    (void)hipGetLastError();
+    int dev = 0;
+    hipError_t e = hipGetDevice(&dev);
+    if (e != hipSuccess) return e;
+    const uint64_t bit = dev < 64 ? (uint64_t)1 << dev : 0;   // (past 64: each time)
+    if (done.load(std::memory_order_relaxed) & bit) return hipSuccess;
+    e = hipFuncSetAttribute(reinterpret_cast<const void*>(kern), hipFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+    if (e == hipSuccess) done.fetch_or(bit, std::memory_order_relaxed);
+    else (void)hipGetLastError();
     return e;
 }
 
@@ -523,7 +581,8 @@ hipError_t launch_delta_walk(const DeltaParams& p, hipStream_t stream)
     using Cf = WalkCfg<IO, N, false>;
     auto* const kern = &delta_walk_kernel<IO, N>;
     static_assert(Cf::total <= 160 * 1024, "a workgroup's LDS");
-    static const hipError_t attr = delta_allow_lds(kern, Cf::total);
+    static std::atomic<uint64_t> done{0};
+    const hipError_t attr = delta_allow_lds(kern, Cf::total, done);
     if (attr != hipSuccess) return attr;
     const int64_t blocks = ((int64_t)p.rows * p.H + 7) / 8 * 8 * (p.P / 16);
     const size_t lds = Cf::total;
