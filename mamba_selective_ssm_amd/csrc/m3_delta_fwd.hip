@@ -12,20 +12,21 @@ namespace {
 // 53 us at 256 slices, 2048 tokens, N = 64.  With more, a CU's LDS reads are,
 // and delta_wide has a quarter of them (whole calls over 2048 tokens, us, P =
 // 64, delta_walk / delta_wide): N = 64: 288 slices 104 / 100, 384: 112 / 107,
-// 512: 128 / 122, 544: 170 / 128, 768: 264 / 190, 1024: 337 / 237; N = 32, 512:
-// 113 / 97; N = 128, 288: 130 / 122, 512: 183 / 151, 1024: 368 / 312.  Where P
-// and the LDS allow, 64 columns go to a workgroup: with 32 of them the calls
-// above 512 slices are two rounds over the chip (N = 64: 544: 185, 768: 245,
-// 1024: 281 us), those up to 512 take the same time.
+// 512: 128 / 118, 768: 264 / 186, 1024: 337 / 230; N = 32, 512: 113 / 97; N =
+// 128, 288: 130 / 125, 512: 183 / 162, 1024: 368 / 266.  Where P allows, 64
+// columns go to a workgroup above 512 slices: with 32 of them such calls are two
+// rounds over the chip or more (N = 64: 544 slices 185 for 128, 768: 245 for
+// 186, 1024: 281 for 230; N = 128, 1024: 309 for 266).  Up to there half of the
+// CUs would be idle with 64 (N = 128, 512 slices: 166 for 162).
 template <typename IO, int N>
 hipError_t fwd_n(const DeltaParams& p, hipStream_t stream)
 {
     const hipError_t e = launch_delta_chunks<IO, N, false>(p, stream);
     if (e != hipSuccess) return e;
     if constexpr (sizeof(IO) == 2) {
-        if ((int64_t)p.rows * p.H * (p.P / 16) > 256) {
-            if constexpr (N < 128)
-                if (p.P % 64 == 0) return launch_delta_wide<N, 4>(p, stream);
+        const int64_t slices = (int64_t)p.rows * p.H * (p.P / 16);
+        if (slices > 256) {
+            if (p.P % 64 == 0 && slices > 512) return launch_delta_wide<N, 4>(p, stream);
             return launch_delta_wide<N, 2>(p, stream);
         }
     }

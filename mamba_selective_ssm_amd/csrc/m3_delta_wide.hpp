@@ -12,19 +12,24 @@ namespace m3 {
 // one's second operand as it lies, so neither LDS nor a barrier stands between
 // the products.  A step takes it longer than four wavefronts together (four
 // times their products), but it reads a quarter of what they read from LDS,
-// which is what bounds a CU that runs several of them, and one K, T and
-// set of factors serves NS of them.  The state waves leave the planes of S and U
-// for four output waves, which work one chunk behind, each on one row tile of
-// all column groups, so that Q and A are read once; one barrier a chunk.  bf16
-// calls only: K's planes of a float32 call would leave no room.  Bound by its
-// chain and by LDS: 237 us a call (1.1 TB/s of the call's own bytes) at 8 x 32
-// heads x 2048 tokens, N = P = 64, where delta_walk takes 337.
+// which is what bounds a CU that runs several of them, and one K, T and set of
+// factors serves NS of them.  The state waves leave the planes of S and U for
+// four output waves, each with two row tiles of half the column groups (all
+// groups of one tile read twice as much LDS, and buffers twice as large left no
+// room for NS = 4 at N = 128: 508 for 375 us there, below); Q S beside R and U,
+// A U beside the state's product, two barriers a chunk.  bf16 calls only: K's
+// planes of a float32 call would leave no room.
+// 8 x 32 heads x 2048 tokens, P = 64: 230 us a call at N = 64 (delta_walk 337),
+// of which 150 are this kernel's; 266 at N = 128 (368), where its 650 MB move at
+// 4 TB/s.  13 packed sequences of 20011 tokens, 32 heads, N = P = 128: 375 us,
+// 5 us a chunk and CU: matrix cores busy for 33% of them, vector units 31%, LDS
+// 31% and 10% in bank conflicts, the chain's waits the rest.
 template <int N, int NS> struct WideCfg {
     static constexpr int WP = DeltaPlanes<bf16>::wide, OP = DeltaPlanes<bf16>::out;
     static constexpr int KB = N / 32, NT = N / 16, waves = NS + 5;
-    // bytes of one of two buffers, then per column group the planes of S and U, twice
+    // bytes of one of two buffers, then per column group the planes of S and U
     static constexpr int k = 0, t = k + 64 * N * 2, f = t + kTriBlocks * WP * 1024, v = f + 5 * 256, buf = v + 64 * NS * 32;
-    static constexpr int ex = 2 * buf, u = OP * KB * 1024, ex1 = u + OP * 2048, total = ex + 2 * NS * ex1;
+    static constexpr int ex = 2 * buf, u = OP * KB * 1024, ex1 = u + OP * 2048, total = ex + NS * ex1;
 };
 
 template <int N, int NS>
@@ -53,6 +58,15 @@ __global__ __launch_bounds__(64 * (NS + 5)) void delta_wide_kernel(const DeltaPa
     const int nlast = (int)(row.len - (int64_t)(nch - 1) * kDC);   // tokens of the last chunk
     const f32x4 fz = {0.f, 0.f, 0.f, 0.f};
 
+    // what this wavefront has written to LDS is there, and s_barrier alone: the
+    // release of __syncthreads would wait for loads and stores too
+    auto bar = [&]() {
+        asm volatile("" ::: "memory");
+        __builtin_amdgcn_s_waitcnt(15 | (3 << 14) | (7 << 4));
+        __builtin_amdgcn_s_barrier();
+        asm volatile("" ::: "memory");
+    };
+
     if (wave == NS + 4) {   // loader: chunk c + 1 beside chunk c
         const bf16* kp = reinterpret_cast<const bf16*>(p.k) + (row.start * p.G + h / (p.H / p.G)) * N;
         const bf16* vp = reinterpret_cast<const bf16*>(p.v) + (row.start * p.H + h) * p.P + p0;
@@ -78,89 +92,104 @@ __global__ __launch_bounds__(64 * (NS + 5)) void delta_wide_kernel(const DeltaPa
 #pragma unroll
             for (int i = 0; i < kTriBlocks * WP; ++i) to_lds16(buf + Cf::t + 1024 * i, tsrc + 1024 * i + 16 * lane);
         };
-        auto barrier = [&]() {
-            asm volatile("" ::: "memory");
-            __builtin_amdgcn_s_waitcnt(0);
-            __builtin_amdgcn_s_barrier();
-            asm volatile("" ::: "memory");
-        };
         if (nch > 0) stage(0);
-        barrier();
+        __builtin_amdgcn_s_waitcnt(0);
+        bar();
         for (int c = 0; c < nch; ++c) {
             if (c + 1 < nch) stage(c + 1);
-            barrier();
+            bar();   // U
+            asm volatile("" ::: "memory");
+            __builtin_amdgcn_s_waitcnt(0);
+            bar();   // S
         }
         return;
     }
 
-    if (wave >= NS) {   // output: row tile w of chunk c beside the state's chunk c + 1, as O^T
-        // (NB: 32-token blocks that the tile of A spans.)  No load depends on a
-        // branch: where one might, a wait for the chunk's operands would also
-        // wait for those of the chunk after it.
-        auto output = [&](auto blocks) {
-            constexpr int NB = decltype(blocks)::value;
-            const int w = wave - NS;
-            const int t = tile_row(w, l);   // this lane's token
-            const bf16* qp = reinterpret_cast<const bf16*>(p.q) + (row.start * p.G + h / (p.H / p.G)) * N + 8 * g;
-            bf16* op = reinterpret_cast<bf16*>(p.o) + (row.start * p.H + h) * p.P + p0 + 4 * g;
-            bf16x8 q[KB][1], a[NB][OP];
-            float fo;
-            auto load = [&](int c) {
-                c = c < nch ? c : nch - 1;
-                const int end = c == nch - 1 ? nlast - 1 : kDC - 1;
-                const bf16* qc = qp + (int64_t)c * kDC * rs + (t < end ? t : end) * rs;
+    if (wave >= NS) {   // output, as O^T: two row tiles of half the column groups
+        const int w = wave - NS;
+        const int tile[2] = {w & 1, 3 - (w & 1)};   // A spans one 32-token block there, and two
+        constexpr int NG = NS / 2;
+        const int cg0 = (w >> 1) * NG;
+        const int t[2] = {tile_row(tile[0], l), tile_row(tile[1], l)};   // this lane's tokens
+        const bf16* qp = reinterpret_cast<const bf16*>(p.q) + (row.start * p.G + h / (p.H / p.G)) * N + 8 * g;
+        bf16* op = reinterpret_cast<bf16*>(p.o) + (row.start * p.H + h) * p.P + p0 + 16 * cg0 + 4 * g;
+        bf16x8 q[2][KB][1], a[3][OP];
+        float fo[2];
+        // (No load depends on a branch: where one might, a wait for the chunk's
+        // operands would also wait for those of the chunk after it.)
+        auto load_q = [&](int c) {
+            c = c < nch ? c : nch - 1;
+            const int end = c == nch - 1 ? nlast - 1 : kDC - 1;
 #pragma unroll
-                for (int kb = 0; kb < KB; ++kb) q[kb][0] = *reinterpret_cast<const bf16x8*>(qc + 32 * kb);
-                const bf16* src = p.af + (ci0 + (int64_t)c * p.H) * (kTriBlocks * OP * 512) + lane * 8;
+            for (int i = 0; i < 2; ++i) {
+                const bf16* qc = qp + (int64_t)c * kDC * rs + (t[i] < end ? t[i] : end) * rs;
 #pragma unroll
-                for (int kb = 0; kb < NB; ++kb)
-#pragma unroll
-                    for (int j = 0; j < OP; ++j)
-                        a[kb][j] = *reinterpret_cast<const bf16x8*>(src + (low_block(w, kb) * OP + j) * 512);
-                fo = p.sc[(ci0 + (int64_t)c * p.H) * (kDScal * 64) + 192 + t];
-            };
-            if (nch > 0) load(0);
-            __syncthreads();
-            for (int c = 0; c < nch; ++c) {
-                __syncthreads();   // the state waves are done with chunk c
-                const char* ex = wlds + Cf::ex + (c & 1) * Cf::ex1 + 16 * lane;
-                f32x4 acc[NS];
-#pragma unroll
-                for (int i = 0; i < NS; ++i) {
-                    const char* e = ex + i * 2 * Cf::ex1;
-                    acc[i] = fz;
-#pragma unroll
-                    for (int kb = 0; kb < KB; ++kb) {
-                        bf16x8 s8[1][OP];
-#pragma unroll
-                        for (int j = 0; j < OP; ++j) s8[0][j] = *reinterpret_cast<const bf16x8*>(e + (j * KB + kb) * 1024);
-                        mma_tiles<1, OP, 1, OP>(s8, q[kb], &acc[i]);
-                    }
-#pragma unroll
-                    for (int r = 0; r < 4; ++r) acc[i][r] *= fo;
-#pragma unroll
-                    for (int kb = 0; kb < NB; ++kb) {
-                        bf16x8 u8[1][OP];
-#pragma unroll
-                        for (int j = 0; j < OP; ++j) u8[0][j] = *reinterpret_cast<const bf16x8*>(e + Cf::u + (2 * j + kb) * 1024);
-                        mma_tiles<1, OP, OP, OP>(u8, a[kb], &acc[i]);
-                    }
-                }
-                load(c + 1);
-                if (t < (c == nch - 1 ? nlast : kDC)) {
-                    bf16* oc = op + ((int64_t)c * kDC + t) * vs;
-#pragma unroll
-                    for (int i = 0; i < NS; ++i) gstore4(oc + 16 * i, acc[i]);
-                }
+                for (int kb = 0; kb < KB; ++kb) q[i][kb][0] = *reinterpret_cast<const bf16x8*>(qc + 32 * kb);
+                fo[i] = p.sc[(ci0 + (int64_t)c * p.H) * (kDScal * 64) + 192 + t[i]];
             }
         };
-        if (wave < NS + 2) output(std::integral_constant<int, 1>());
-        else output(std::integral_constant<int, 2>());
+        auto load_a = [&](int c) {
+            c = c < nch ? c : nch - 1;
+            const bf16* src = p.af + (ci0 + (int64_t)c * p.H) * (kTriBlocks * OP * 512) + lane * 8;
+#pragma unroll
+            for (int j = 0; j < OP; ++j) {
+                a[0][j] = *reinterpret_cast<const bf16x8*>(src + (low_block(tile[0], 0) * OP + j) * 512);
+                a[1][j] = *reinterpret_cast<const bf16x8*>(src + (low_block(tile[1], 0) * OP + j) * 512);
+                a[2][j] = *reinterpret_cast<const bf16x8*>(src + (low_block(tile[1], 1) * OP + j) * 512);
+            }
+        };
+        if (nch > 0) {
+            load_q(0);
+            load_a(0);
+        }
+        bar();
+        const char* ex = wlds + Cf::ex + cg0 * Cf::ex1 + 16 * lane;
+        for (int c = 0; c < nch; ++c) {
+            f32x4 acc[2][NG];
+#pragma unroll
+            for (int i = 0; i < NG; ++i) {
+                acc[0][i] = fz;
+                acc[1][i] = fz;
+#pragma unroll
+                for (int kb = 0; kb < KB; ++kb) {
+                    bf16x8 s8[1][OP];
+#pragma unroll
+                    for (int j = 0; j < OP; ++j) s8[0][j] = *reinterpret_cast<const bf16x8*>(ex + i * Cf::ex1 + (j * KB + kb) * 1024);
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) mma_tiles<1, OP, 1, OP>(s8, q[k][kb], &acc[k][i]);
+                }
+#pragma unroll
+                for (int k = 0; k < 2; ++k)
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) acc[k][i][r] *= fo[k];
+            }
+            load_q(c + 1);
+            bar();   // U
+#pragma unroll
+            for (int i = 0; i < NG; ++i)
+#pragma unroll
+                for (int kb = 0; kb < 2; ++kb) {
+                    bf16x8 u8[1][OP];
+#pragma unroll
+                    for (int j = 0; j < OP; ++j) u8[0][j] = *reinterpret_cast<const bf16x8*>(ex + i * Cf::ex1 + Cf::u + (2 * j + kb) * 1024);
+                    if (kb == 0) mma_tiles<1, OP, OP, OP>(u8, a[0], &acc[0][i]);
+                    mma_tiles<1, OP, OP, OP>(u8, a[1 + kb], &acc[1][i]);
+                }
+            load_a(c + 1);
+#pragma unroll
+            for (int k = 0; k < 2; ++k)
+                if (t[k] < (c == nch - 1 ? nlast : kDC)) {
+                    bf16* oc = op + ((int64_t)c * kDC + t[k]) * vs;
+#pragma unroll
+                    for (int i = 0; i < NG; ++i) gstore4(oc + 16 * i, acc[k][i]);
+                }
+            bar();   // S
+        }
         return;
     }
 
     const int cg = wave;   // column group
-    char* ex0 = wlds + Cf::ex + cg * 2 * Cf::ex1 + 16 * lane;
+    char* ex = wlds + Cf::ex + cg * Cf::ex1 + 16 * lane;
 
     // state: tile i holds rows tile_row(i, 4 g + r) of the state, column l
     const int col = p0 + 16 * cg + l;
@@ -183,15 +212,17 @@ __global__ __launch_bounds__(64 * (NS + 5)) void delta_wide_kernel(const DeltaPa
     bf16x8 s8[KB][WP];
 #pragma unroll
     for (int kb = 0; kb < KB; ++kb) planes_of(S[2 * kb], S[2 * kb + 1], s8[kb]);
-    __syncthreads();
-
-    for (int c = 0; c < nch; ++c) {
-        const char* buf = wlds + (c & 1) * Cf::buf;
-        char* ex = ex0 + (c & 1) * Cf::ex1;
+    auto put_state = [&]() {
 #pragma unroll
         for (int kb = 0; kb < KB; ++kb)
 #pragma unroll
             for (int j = 0; j < OP; ++j) *reinterpret_cast<bf16x8*>(ex + (j * KB + kb) * 1024) = s8[kb][j];
+    };
+    put_state();
+    bar();
+
+    for (int c = 0; c < nch; ++c) {
+        const char* buf = wlds + (c & 1) * Cf::buf;
         // R = beta V - sp (K S)
         f32x4 P[4] = {fz, fz, fz, fz};
 #pragma unroll
@@ -249,6 +280,7 @@ __global__ __launch_bounds__(64 * (NS + 5)) void delta_wide_kernel(const DeltaPa
         }
         planes_of(U[0], U[1], r8[0]);
         planes_of(U[2], U[3], r8[1]);
+        bar();   // U
         // S <- e^G_last S + K^T (d U)
         const float eL = *reinterpret_cast<const float*>(buf + Cf::f + 1024 + 4 * lane);
         constexpr int TN = NT < 4 ? NT : 4;   // tiles in turn
@@ -280,7 +312,8 @@ __global__ __launch_bounds__(64 * (NS + 5)) void delta_wide_kernel(const DeltaPa
                 planes_of(S[i0 + i], S[i0 + i + 1], s8[(i0 + i) / 2]);
             }
         }
-        __syncthreads();
+        put_state();
+        bar();   // S
     }
     if (p.h_out != nullptr && rec >= 0) {
         float* ho = p.h_out + ((rec * p.H + h) * N + 8 * g) * p.P + col;
