@@ -52,6 +52,7 @@ struct DeltaPlan {
     int64_t G, nc, chunks;     // q/k groups; chunks of the longest row; (chunk slot, head) entries
     size_t tri_w, tri_o, sc;   // bytes of one array of each kind
     size_t st, rowsP, heads;   // gradient: states, [64][P] rows, per-head dq or dk
+    size_t order;              // packed rows in the walks' order
     size_t fwd, bwd;           // whole workspaces
 };
 
@@ -88,8 +89,11 @@ m3_status plan_delta(const m3_delta_args* a, bool train, DeltaPlan* out)
     out->rowsP = up256(n * (size_t)(64 * a->headdim) * 4);
     const size_t tokens = (size_t)(packed ? 1 : a->batch) * (size_t)a->seqlen;
     out->heads = out->G == H ? 0 : up256(tokens * (size_t)(H * a->dstate) * 4);
-    out->fwd = n == 0 ? 0 : out->tri_w + out->tri_o + out->sc;
-    out->bwd = n == 0 ? 0 : out->tri_w + out->sc + 2 * out->st + 2 * out->rowsP + 2 * out->heads;
+    // (places are counted row against row: left out where that would show, and
+    // so many rows leave no CU idle for long)
+    out->order = packed && out->nc > 0 && a->batch <= 16384 ? up256((size_t)a->batch * 4) : 0;
+    out->fwd = n == 0 ? 0 : out->tri_w + out->tri_o + out->sc + out->order;
+    out->bwd = n == 0 ? 0 : out->tri_w + out->sc + out->order + 2 * out->st + 2 * out->rowsP + 2 * out->heads;
     return M3_OK;
 }
 
@@ -259,6 +263,7 @@ m3_status m3_delta_fwd(const m3_delta_args* a, void* stream)
     p.tf = reinterpret_cast<m3::bf16*>(w);
     p.af = reinterpret_cast<m3::bf16*>(w + pl.tri_w);
     p.sc = reinterpret_cast<float*>(w + pl.tri_w + pl.tri_o);
+    if (pl.order > 0) p.order = reinterpret_cast<int*>(w + pl.tri_w + pl.tri_o + pl.sc);
     return status_of(m3::launch_delta_fwd(p, a->io_dtype, static_cast<hipStream_t>(stream)));
 }
 
@@ -340,6 +345,7 @@ m3_status m3_delta_bwd(const m3_delta_bwd_args* b, void* stream)
     auto take = [&w](size_t bytes) { char* x = w; w += bytes; return x; };
     p.f.tf = reinterpret_cast<m3::bf16*>(take(pl.tri_w));
     p.f.sc = reinterpret_cast<float*>(take(pl.sc));
+    if (pl.order > 0) p.f.order = reinterpret_cast<int*>(take(pl.order));
     p.S = reinterpret_cast<float*>(take(pl.st));
     p.dS = reinterpret_cast<float*>(take(pl.st));
     p.U = reinterpret_cast<float*>(take(pl.rowsP));

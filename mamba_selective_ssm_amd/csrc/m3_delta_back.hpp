@@ -211,9 +211,10 @@ __device__ __forceinline__ void delta_back(const DeltaBwdParams& bp, int64_t bid
     const int64_t idx = bid >> 3;
     const int64_t unit = (idx / nsl) * 8 + (bid & 7);
     if (unit >= (int64_t)p.rows * p.H) return;
-    int64_t b64, h64;
-    split_bh(unit, p.H, b64, h64);
-    const int b = (int)b64, h = (int)h64, p0 = (int)(idx % nsl) * 16;
+    int b, h;
+    delta_unit(p, unit, b, h);
+    const int64_t rec = (int64_t)b * p.H + h;
+    const int p0 = (int)(idx % nsl) * 16;
     const DeltaRow row = delta_row(p, b);
     const int nch = (int)((row.len + kDC - 1) / kDC);
     const int64_t ci0 = row.slot0 * p.H + h;
@@ -227,7 +228,7 @@ __device__ __forceinline__ void delta_back(const DeltaBwdParams& bp, int64_t bid
     const int tr0 = 32 * (w >> 1) + 4 * (w & 1) + 8 * g, half = 8 * (w & 1), col = p0 + l, P = p.P;
     const int kb0 = w >> 1;   // first 32-token block of this wave's rows of T^T
     f32x4 S[TI];
-    const float* hin = bp.dh_out != nullptr ? bp.dh_out + unit * (int64_t)(N * P) + col : nullptr;
+    const float* hin = bp.dh_out != nullptr ? bp.dh_out + rec * (int64_t)(N * P) + col : nullptr;
 #pragma unroll
     for (int i = 0; i < TI; ++i)
 #pragma unroll
@@ -375,7 +376,7 @@ __device__ __forceinline__ void delta_back(const DeltaBwdParams& bp, int64_t bid
         __syncthreads();
     }
     if (bp.dh_in != nullptr) {
-        float* ho = bp.dh_in + unit * (int64_t)(N * P) + col;
+        float* ho = bp.dh_in + rec * (int64_t)(N * P) + col;
 #pragma unroll
         for (int i = 0; i < TI; ++i)
             if (w + 4 * i < NT)

@@ -107,6 +107,7 @@ __global__ __launch_bounds__(64, 2) void delta_chunk_kernel(const DeltaParams p)
     const int h = (int)(bid % p.H);
     const int bc = (int)(bid / p.H);
     const int c = bc % p.nc, b = bc / p.nc;
+    if (c == 0 && h == 0 && p.order != nullptr) delta_rank(p, b, lane);
     const DeltaRow row = delta_row(p, b);
     if ((int64_t)c * kDC >= row.len) return;
     const int64_t t0 = row.start + (int64_t)c * kDC;

@@ -241,9 +241,8 @@ __device__ __forceinline__ void delta_walk(const DeltaParams& p, float* Sbuf, fl
     const int64_t idx = bid >> 3;
     const int64_t unit = (idx / nsl) * 8 + (bid & 7);
     if (unit >= (int64_t)p.rows * p.H) return;
-    int64_t b64, h64;
-    split_bh(unit, p.H, b64, h64);
-    const int b = (int)b64, h = (int)h64;
+    int b, h;
+    delta_unit(p, unit, b, h);
     const int p0 = (int)(idx % nsl) * 16;   // first column
     const DeltaRow row = delta_row(p, b);
     const int64_t rec = TRAIN ? b : delta_record(p, b, tid, 64 * Cf::waves, reinterpret_cast<int*>(wlds));

@@ -46,9 +46,8 @@ __global__ __launch_bounds__(64 * (NS + 5)) void delta_wide_kernel(const DeltaPa
     const int64_t idx = blockIdx.x >> 3;
     const int64_t unit = (idx / nsl) * 8 + (blockIdx.x & 7);
     if (unit >= (int64_t)p.rows * p.H) return;
-    int64_t b64, h64;
-    split_bh(unit, p.H, b64, h64);
-    const int b = (int)b64, h = (int)h64;
+    int b, h;
+    delta_unit(p, unit, b, h);
     const int p0 = (int)(idx % nsl) * (16 * NS);
     const DeltaRow row = delta_row(p, b);
     const int64_t rec = delta_record(p, b, tid, 64 * Cf::waves, reinterpret_cast<int*>(wlds));

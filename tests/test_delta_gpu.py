@@ -363,3 +363,25 @@ def test_refused_sizes():
     x = ref.inputs(1, 10, 2, 2, 48, 64, torch.bfloat16, 181)
     with pytest.raises(M3Error):
         m3_delta_fwd(*x)
+
+
+@pytest.mark.parametrize("rows", [700, 16384, 16385])
+def test_many_short_sequences(rows):
+    """Packed rows are walked in the order of their lengths, above 16384 rows as they stand: each row's result is that of
+    the recurrence on the rows of its length."""
+    H, N, P = 1, 32, 32
+    lens = torch.tensor([(5, 1, 70, 0, 2)[i % 5] if i < 500 else (1, 2, 0)[i % 3] for i in range(rows)])
+    T = int(lens.sum())
+    x = ref.inputs(1, T, H, H, N, P, torch.bfloat16, 61)
+    cu = torch.cat([torch.zeros(1, dtype=torch.int64), lens.cumsum(0)])
+    h = torch.randn(rows, H, N, P, generator=torch.Generator().manual_seed(62)).cuda()
+    o, hL = m3_delta_fwd(*x, h, l2norm=True, cu_seqlens=cu.to(torch.int32).cuda(), max_seqlen=int(lens.max()))
+    for n in lens.unique().tolist():
+        at = (lens == n).nonzero()[:, 0]
+        if n == 0:
+            assert torch.equal(hL[at.cuda()], h[at.cuda()])
+            continue
+        tok = (cu[at][:, None] + torch.arange(n)).cuda()
+        wo, wh = ref.forward(*(t[0][tok] for t in x), h[at.cuda()], scale=N ** -0.5, l2norm=True)
+        check_o(o[0][tok], wo, "bf16", "length %d" % n)
+        check_h(hL[at.cuda()], wh, "length %d" % n)
