@@ -44,7 +44,10 @@ struct DeltaParams {
     int N, P;
     float scale, eps;
     int l2norm;
-    int nc;                // chunks of the longest row
+    int nc;                // chunks of the longest row, or of the part
+    int64_t from, count;   // the part of each row that a launch works on, in chunks (count 0: all of it)
+    const float* carry_in; // [rows][H][N][P] state before that part where it is not the row's first, else NULL
+    float* carry_out;      // and behind it where it is not the last
     // workspace, one entry per (chunk slot, head)
     bf16* tf;              // T in operand order
     bf16* af;              // scale D o Q K^T in operand order
@@ -74,6 +77,16 @@ constexpr bool delta_supported(int64_t N, int64_t P, int io_dtype)
 {
     return (N == 32 || N == 64 || N == 128) && P >= 32 && P <= 128 && P % 32 == 0 && (io_dtype == 0 || io_dtype == 1);
 }
+
+// Long prefills whose walk leaves CUs idle are walked in parts, each beside the
+// chunk matrices of the next, which the walk then reads out of the caches.  Whole
+// calls, us, at once / in parts: 65536 tokens, 128 slices, N = 128: 2094 / 1985;
+// 16384: 552 / 472; N = 64, 65536 tokens, 32 slices: 1598 / 1190; 32768, 64: 872 /
+// 662; 160: 1156 / 1090; 192: 1100 / 1050; 256: 1182 / 1238.  A part has to be
+// long beside a launch and the walk's first loads: 8192 tokens (parts of 16
+// chunks), N = 64: 152 / 182.  16 parts take the same times as 8, 4 more.
+constexpr int kDeltaParts = 8;
+constexpr bool delta_in_parts(int64_t units, int64_t nc, int64_t P) { return units * (P / 16) <= 192 && nc >= 32 * kDeltaParts; }
 
 // Planes of float32 operands on the state's path and on the output's path, and
 // of the io type's own values.  The output of a bf16 call is rounded to bf16
@@ -117,7 +130,7 @@ __device__ __forceinline__ DeltaRow delta_row(const DeltaParams& p, int b)
     if (p.cu == nullptr) {
         r.start = (int64_t)b * p.L;
         r.len = p.L;
-        r.slot0 = (int64_t)b * p.nc;
+        r.slot0 = (int64_t)b * ((p.L + kDC - 1) / kDC);
     } else {
         int64_t s = p.cu[b], e = p.cu[b + 1];
         s = s < 0 ? 0 : (s > p.L ? p.L : s);
@@ -126,6 +139,12 @@ __device__ __forceinline__ DeltaRow delta_row(const DeltaParams& p, int b)
         r.len = e - s < p.max_len ? e - s : p.max_len;
         // floor(a + b) + 1 >= floor(a) + ceil(b): no two rows share a slot
         r.slot0 = s / kDC + b;
+    }
+    if (p.count > 0) {
+        const int64_t left = r.len - p.from * kDC;
+        r.start += left > 0 ? p.from * kDC : 0;
+        r.slot0 += p.from;
+        r.len = left < 0 ? 0 : left < p.count * kDC ? left : p.count * kDC;
     }
     return r;
 }

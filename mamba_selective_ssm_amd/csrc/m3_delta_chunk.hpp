@@ -94,20 +94,20 @@ template <int PL, int LD> __device__ __forceinline__ void put_lower(bf16* dst, c
 // four wavefronts with shared rows and barriers took 40 and 750 us.  Without A,
 // which the walk would then make, 15.6 and 246 us; but the walk lost more (56
 // for 39 and 1980 for 1660 us).
+constexpr int kChunkLds = (64 * 68 + 5 * 64) * 4;   // bytes
 template <typename IO, int N, bool BWD>
-__global__ __launch_bounds__(64, 2) void delta_chunk_kernel(const DeltaParams p)
+__device__ __forceinline__ void delta_chunk(const DeltaParams& p, int64_t bid, char* lds)
 {
     constexpr int KP = DeltaPlanes<IO>::io, WP = DeltaPlanes<IO>::wide, OP = DeltaPlanes<IO>::out;
     constexpr int KB = N / 32, LD = 68;
-    __shared__ __attribute__((aligned(16))) float sM[64 * LD];
-    __shared__ __attribute__((aligned(16))) float sGh[64], sGl[64], sBk[64], sRk[64], sRq[64];
+    float* sM = reinterpret_cast<float*>(lds);
+    float *sGh = sM + 64 * LD, *sGl = sGh + 64, *sBk = sGl + 64, *sRk = sBk + 64, *sRq = sRk + 64;
 
-    const int lane = threadIdx.x, l = lane & 15, g = lane >> 4;
-    const int64_t bid = blockIdx.x;
+    const int lane = threadIdx.x & 63, l = lane & 15, g = lane >> 4;
     const int h = (int)(bid % p.H);
     const int bc = (int)(bid / p.H);
     const int c = bc % p.nc, b = bc / p.nc;
-    if (c == 0 && h == 0 && p.order != nullptr) delta_rank(p, b, lane);
+    if (c == 0 && h == 0 && p.from == 0 && p.order != nullptr) delta_rank(p, b, lane);
     const DeltaRow row = delta_row(p, b);
     if ((int64_t)c * kDC >= row.len) return;
     const int64_t t0 = row.start + (int64_t)c * kDC;
@@ -332,6 +332,13 @@ __global__ __launch_bounds__(64, 2) void delta_chunk_kernel(const DeltaParams p)
     }
     wave_order();
     put_lower<WP, LD>(p.tf + ci * (kTriBlocks * WP * 512), sM, l, g, lane);
+}
+
+template <typename IO, int N, bool BWD>
+__global__ __launch_bounds__(64, 2) void delta_chunk_kernel(const DeltaParams p)
+{
+    __shared__ __attribute__((aligned(16))) char lds[kChunkLds];
+    delta_chunk<IO, N, BWD>(p, blockIdx.x, lds);
 }
 
 template <typename IO, int N, bool BWD>

@@ -6,6 +6,57 @@ namespace m3 {
 
 namespace {
 
+// A part of every row's chunks is walked beside the next part's chunk matrices:
+// workgroups [0, walks) have the walk, each wavefront of the others a chunk and
+// head.  The walk alone leaves the CUs idle that it has no slices for.
+template <typename IO, int N>
+__global__ __launch_bounds__(64 * 7) void delta_both_kernel(const DeltaParams p, const DeltaParams next, const unsigned walks)
+{
+    extern __shared__ __attribute__((aligned(16))) char wlds[];
+    if (blockIdx.x < walks) {
+        delta_walk<IO, N, false>(p, nullptr, nullptr, blockIdx.x, wlds);
+        return;
+    }
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int64_t unit = (int64_t)(blockIdx.x - walks) * 7 + wave;
+    if (unit < (int64_t)next.rows * next.nc * next.H) delta_chunk<IO, N, false>(next, unit, wlds + wave * kChunkLds);
+}
+
+template <typename IO, int N>
+hipError_t launch_delta_parts(const DeltaParams& p, hipStream_t stream)
+{
+    using Cf = WalkCfg<IO, N, false>;
+    static_assert(Cf::waves == 7, "a wavefront to each of delta_both_kernel's chunks");
+    constexpr size_t lds = Cf::total > 7 * kChunkLds ? Cf::total : 7 * kChunkLds;
+    static_assert(lds <= 160 * 1024, "a workgroup's LDS");
+    auto* const kern = &delta_both_kernel<IO, N>;
+    static std::atomic<uint64_t> done{0};
+    hipError_t e = delta_allow_lds(kern, lds, done);
+    if (e != hipSuccess) return e;
+    const int64_t each = (p.nc + kDeltaParts - 1) / kDeltaParts;
+    auto part = [&](int64_t from) {
+        DeltaParams q = p;
+        q.from = from;
+        q.count = each;
+        q.nc = (int)(p.nc - from < each ? p.nc - from : each);
+        if (from == 0) q.carry_in = nullptr;
+        if (from + each >= p.nc) q.carry_out = nullptr;
+        return q;
+    };
+    if ((e = launch_delta_chunks<IO, N, false>(part(0), stream)) != hipSuccess) return e;
+    const unsigned walks = (unsigned)(((int64_t)p.rows * p.H + 7) / 8 * 8 * (p.P / 16));
+    for (int64_t c = 0; c < p.nc; c += each) {
+        const DeltaParams now = part(c);
+        DeltaParams next = now;
+        next.nc = 0;
+        if (c + each < p.nc) next = part(c + each);
+        const unsigned chunks = (unsigned)(((int64_t)p.rows * next.nc * p.H + 6) / 7);
+        hipLaunchKernelGGL(kern, dim3(walks + chunks), dim3(64 * 7), lds, stream, now, next, walks);
+        if ((e = hipGetLastError()) != hipSuccess) return e;
+    }
+    return hipSuccess;
+}
+
 // Which walk.  A slice is 16 columns of one row and head.  Up to one slice per
 // CU its chain of products is the call's time, and four wavefronts on one slice
 // (delta_walk) take less than one wavefront's registers (delta_wide): 39 against
@@ -21,6 +72,7 @@ namespace {
 template <typename IO, int N>
 hipError_t fwd_n(const DeltaParams& p, hipStream_t stream)
 {
+    if (p.carry_out != nullptr) return launch_delta_parts<IO, N>(p, stream);
     const hipError_t e = launch_delta_chunks<IO, N, false>(p, stream);
     if (e != hipSuccess) return e;
     if constexpr (sizeof(IO) == 2) {

@@ -385,6 +385,7 @@ __device__ __forceinline__ void delta_walk(const DeltaParams& p, float* Sbuf, fl
     const int col = p0 + l;
     f32x4 S[TI];
     const float* hin = p.h_in != nullptr && rec >= 0 ? p.h_in + (rec * p.H + h) * (int64_t)(N * p.P) + col : nullptr;
+    if (!TRAIN && p.carry_in != nullptr) hin = p.carry_in + ((int64_t)b * p.H + h) * (int64_t)(N * p.P) + col;
 #pragma unroll
     for (int i = 0; i < TI; ++i)
 #pragma unroll
@@ -542,8 +543,9 @@ __device__ __forceinline__ void delta_walk(const DeltaParams& p, float* Sbuf, fl
         put_state();
         __syncthreads();
     }
-    if (!TRAIN && p.h_out != nullptr && rec >= 0) {
-        float* ho = p.h_out + (rec * p.H + h) * (int64_t)(N * p.P) + col;
+    float* ho = !TRAIN && p.h_out != nullptr && rec >= 0 ? p.h_out + (rec * p.H + h) * (int64_t)(N * p.P) + col : nullptr;
+    if (!TRAIN && p.carry_out != nullptr) ho = p.carry_out + ((int64_t)b * p.H + h) * (int64_t)(N * p.P) + col;
+    if (ho != nullptr) {
 #pragma unroll
         for (int i = 0; i < TI; ++i)
             if (w + 4 * i < NT)

@@ -58,7 +58,7 @@ __global__ __launch_bounds__(64 * (NS + 5)) void delta_wide_kernel(const DeltaPa
     const f32x4 fz = {0.f, 0.f, 0.f, 0.f};
 
     // what this wavefront has written to LDS is there, and s_barrier alone: the
-    // release of __syncthreads would wait for loads and stores too
+    // release of __syncthreads would also wait for the loader's loads
     auto bar = [&]() {
         asm volatile("" ::: "memory");
         __builtin_amdgcn_s_waitcnt(15 | (3 << 14) | (7 << 4));

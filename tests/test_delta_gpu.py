@@ -385,3 +385,41 @@ def test_many_short_sequences(rows):
         wo, wh = ref.forward(*(t[0][tok] for t in x), h[at.cuda()], scale=N ** -0.5, l2norm=True)
         check_o(o[0][tok], wo, "bf16", "length %d" % n)
         check_h(hL[at.cuda()], wh, "length %d" % n)
+
+
+@pytest.mark.parametrize("io,N,P,B,H,L", [("f32", 32, 32, 2, 3, 16500), ("bf16", 128, 32, 3, 2, 16384), ("bf16", 64, 64, 1, 2, 16449)])
+def test_long_in_parts(io, N, P, B, H, L):
+    """Rows of 256 chunks and more on few CUs: the walk runs in parts that hand on the state."""
+    say("case parts", io, N, P, B, H, L)
+    x = ref.inputs(B, L, H, H, N, P, DT[io], 71)
+    h = torch.randn(B, H, N, P, generator=torch.Generator().manual_seed(72)).cuda()
+    wo, wh = ref.forward(*x, h, scale=0.2, l2norm=True)
+    hl = h.clone()
+    o, _ = m3_delta_fwd(*x, hl, h_out=hl, l2norm=True, scale=0.2)
+    check_o(o, wo, io, "parts")
+    check_h(hl, wh, "parts")
+    again, none = m3_delta_fwd(*x, h, l2norm=True, scale=0.2, return_state=False)
+    assert none is None and torch.equal(again, o)
+
+
+def test_long_packed_in_parts():
+    """Rows that end in the first part and in later ones; records in slots, one row without a record, a slot named twice."""
+    N, P, H = 64, 64, 1
+    lens, slots = [16400, 70, 0, 100, 4200, 16390], [2, 0, 5, 2, 3, -1]
+    x = ref.inputs(1, sum(lens), H, H, N, P, torch.bfloat16, 81)
+    pool = torch.randn(6, H, N, P, generator=torch.Generator().manual_seed(82)).cuda()
+    before = pool.clone()
+    cu = torch.tensor([0] + lens).cumsum(0).to(torch.int32)
+    o, _ = m3_delta_fwd(*x, pool, l2norm=True, scale=0.2, cu_seqlens=cu.cuda(), max_seqlen=16400,
+                        slots=torch.tensor(slots, dtype=torch.int32).cuda())
+    for i, (n, s) in enumerate(zip(lens, slots)):
+        part = slice(int(cu[i]), int(cu[i + 1]))
+        if i == 3:
+            assert bool(o[0, part].isnan().all())
+            continue
+        wo, wh = ref.forward(*(t[:, part] for t in x), before[s:s + 1] if s >= 0 else None, scale=0.2, l2norm=True)
+        check_o(o[:, part], wo, "bf16", "row %d" % i)
+        if s >= 0:
+            check_h(pool[s:s + 1], wh, "row %d" % i)
+    for s in (1, 4, 5):
+        assert torch.equal(pool[s], before[s])
