@@ -495,7 +495,8 @@ m3_status m3_delta_fwd(const m3_delta_args *args, void *stream);
 m3_status m3_delta_step(const m3_delta_step_args *args, void *stream);
 m3_status m3_delta_bwd(const m3_delta_bwd_args *args, void *stream);
 /* Workspace bytes of the calls; 0 for arguments they would reject.  They
- * depend on sizes, io dtype and on whether cu_seqlens is given. */
+ * depend on sizes (not on max_seqlen), io dtype and on whether cu_seqlens is
+ * given. */
 size_t m3_delta_workspace_bytes(const m3_delta_args *args);
 size_t m3_delta_bwd_workspace_bytes(const m3_delta_bwd_args *args);
 /* 1 when (dstate, headdim, io_dtype) is in the compiled set of the three. */

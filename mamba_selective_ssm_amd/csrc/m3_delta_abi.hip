@@ -54,6 +54,7 @@ struct DeltaPlan {
     size_t st, rowsP, heads;   // gradient: states, [64][P] rows, per-head dq or dk
     size_t order;              // packed rows in the walks' order
     size_t carry;              // states between a long prefill's parts
+    bool parts;                // whether it has them
     size_t fwd, bwd;           // whole workspaces
 };
 
@@ -92,8 +93,12 @@ m3_status plan_delta(const m3_delta_args* a, bool train, DeltaPlan* out)
     out->heads = out->G == H ? 0 : up256(tokens * (size_t)(H * a->dstate) * 4);
     // (places are counted row against row: left out where that would show, and
     // so many rows leave no CU idle for long)
-    out->order = packed && out->nc > 0 && a->batch <= 16384 ? up256((size_t)a->batch * 4) : 0;
-    out->carry = m3::delta_in_parts(a->batch * H, out->nc, a->headdim) ? up256((size_t)(a->batch * H * a->dstate * a->headdim) * 4) : 0;
+    out->order = packed && a->batch <= 16384 ? up256((size_t)a->batch * 4) : 0;
+    // (sized for any max_seqlen)
+    out->parts = m3::delta_in_parts(a->batch * H, out->nc, a->headdim);
+    out->carry = m3::delta_in_parts(a->batch * H, (a->seqlen + m3::kDC - 1) / m3::kDC, a->headdim)
+                     ? up256((size_t)(a->batch * H * a->dstate * a->headdim) * 4)
+                     : 0;
     out->fwd = n == 0 ? 0 : out->tri_w + out->tri_o + out->sc + out->order + out->carry;
     out->bwd = n == 0 ? 0 : out->tri_w + out->sc + out->order + 2 * out->st + 2 * out->rowsP + 2 * out->heads;
     return M3_OK;
@@ -265,8 +270,8 @@ m3_status m3_delta_fwd(const m3_delta_args* a, void* stream)
     p.tf = reinterpret_cast<m3::bf16*>(w);
     p.af = reinterpret_cast<m3::bf16*>(w + pl.tri_w);
     p.sc = reinterpret_cast<float*>(w + pl.tri_w + pl.tri_o);
-    if (pl.order > 0) p.order = reinterpret_cast<int*>(w + pl.tri_w + pl.tri_o + pl.sc);
-    if (pl.carry > 0) p.carry_in = p.carry_out = reinterpret_cast<float*>(w + pl.tri_w + pl.tri_o + pl.sc + pl.order);
+    if (pl.order > 0 && pl.nc > 0) p.order = reinterpret_cast<int*>(w + pl.tri_w + pl.tri_o + pl.sc);
+    if (pl.parts) p.carry_in = p.carry_out = reinterpret_cast<float*>(w + pl.tri_w + pl.tri_o + pl.sc + pl.order);
     return status_of(m3::launch_delta_fwd(p, a->io_dtype, static_cast<hipStream_t>(stream)));
 }
 
@@ -348,7 +353,8 @@ m3_status m3_delta_bwd(const m3_delta_bwd_args* b, void* stream)
     auto take = [&w](size_t bytes) { char* x = w; w += bytes; return x; };
     p.f.tf = reinterpret_cast<m3::bf16*>(take(pl.tri_w));
     p.f.sc = reinterpret_cast<float*>(take(pl.sc));
-    if (pl.order > 0) p.f.order = reinterpret_cast<int*>(take(pl.order));
+    int* const order = reinterpret_cast<int*>(take(pl.order));
+    p.f.order = pl.order > 0 && pl.nc > 0 ? order : nullptr;
     p.S = reinterpret_cast<float*>(take(pl.st));
     p.dS = reinterpret_cast<float*>(take(pl.st));
     p.U = reinterpret_cast<float*>(take(pl.rowsP));

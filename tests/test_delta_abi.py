@@ -250,6 +250,15 @@ def test_binding_refusals():
         m3_pool_free(torch.zeros(4, dtype=torch.int32), torch.zeros(1, dtype=torch.int32))
 
 
+def test_workspace_of_long_packed_calls(lib):
+    """One that a call with a long max_seqlen takes is what one with a short max_seqlen asks for."""
+    kw = dict(batch=1, nheads=2, ngroups=2, seqlen=1 << 15, cu_seqlens=at(9))
+    for f in (lambda a: lib.m3_delta_workspace_bytes(ctypes.byref(a)),
+              lambda a: lib.m3_delta_bwd_workspace_bytes(ctypes.byref(delta.DeltaBwdArgs(in_=a)))):
+        need = [f(fwd_args(max_seqlen=n, **kw)) for n in (0, 1, 64, 16383, 16385, 1 << 15)]
+        assert min(need) == max(need) > 0
+
+
 LAUNCH = [   # launches count their threads in 32 bits: the first size that does not fit, and the last that does
     ("fwd", dict(nheads=1 << 10, ngroups=0, headdim=128), "batch", (((1 << 32) - 1) // 448 // 8) // (1 << 10) + 1),
     ("bwd", dict(nheads=1 << 10, ngroups=0, headdim=128), "batch", (((1 << 32) - 1) // 640 // 8) // (1 << 10) + 1),
