@@ -80,13 +80,28 @@ constexpr bool delta_supported(int64_t N, int64_t P, int io_dtype)
 
 // Long prefills whose walk leaves CUs idle are walked in parts, each beside the
 // chunk matrices of the next, which the walk then reads out of the caches.  Whole
-// calls, us, at once / in parts: 65536 tokens, 128 slices, N = 128: 2094 / 1985;
-// 16384: 552 / 472; N = 64, 65536 tokens, 32 slices: 1598 / 1190; 32768, 64: 872 /
-// 662; 160: 1156 / 1090; 192: 1100 / 1050; 256: 1182 / 1238.  A part has to be
-// long beside a launch and the walk's first loads: 8192 tokens (parts of 16
-// chunks), N = 64: 152 / 182.  16 parts take the same times as 8, 4 more.
-constexpr int kDeltaParts = 8;
-constexpr bool delta_in_parts(int64_t units, int64_t nc, int64_t P) { return units * (P / 16) <= 192 && nc >= 32 * kDeltaParts; }
+// calls, us, at once / in parts, P = 64, bf16: 65536 tokens, 128 slices, N = 128:
+// 2092 / 1830; 16384: 553 / 471; 8192: 268 / 236; 4096: 120 / 118; N = 64, 65536
+// tokens, 32 slices: 1594 / 1162, 64: 1700 / 1305; 8192, 192: 296 / 253; at 256
+// slices no CU is left: 1182 / 1238.
+// A part is as many chunks as leave its rows and matrices in the caches together
+// with the next one's, about 1024 chunks and heads in bf16: 32 heads, N = 128,
+// parts of 16 / 32 / 48 / 64 / 128 chunks: 1851 / 1830 / 1941 / 1988 / 1985 us;
+// float32, 16 heads, N = 64, 16384 tokens: 641 / 595 / 625 / 638 (at once: 751).
+// It has to be long beside a launch and the walk's first loads, 32 chunks at
+// least: 16 heads, N = 64, 16384 tokens: 348 / 303 / 295 / 284 (at once: 289).
+// Calls of two such parts or less lie in the caches as they are: 1 head, N = 64,
+// 32768 tokens: 492 / 525; 16 heads, float32, 4096: 164 / 167.
+constexpr int64_t delta_part_size(int io_dtype) { return io_dtype == 0 ? 512 : 1024; }
+constexpr int64_t delta_part(int64_t units, int io_dtype)
+{
+    const int64_t n = delta_part_size(io_dtype) / (units > 0 ? units : 1);
+    return n < 32 ? 32 : n > 64 ? 64 : n;
+}
+constexpr bool delta_in_parts(int64_t units, int64_t nc, int64_t P, int io_dtype)
+{
+    return units * (P / 16) <= 192 && nc >= 2 * delta_part(units, io_dtype) && units * nc > 2 * delta_part_size(io_dtype);
+}
 
 // Planes of float32 operands on the state's path and on the output's path, and
 // of the io type's own values.  The output of a bf16 call is rounded to bf16

@@ -95,8 +95,8 @@ m3_status plan_delta(const m3_delta_args* a, bool train, DeltaPlan* out)
     // so many rows leave no CU idle for long)
     out->order = packed && a->batch <= 16384 ? up256((size_t)a->batch * 4) : 0;
     // (sized for any max_seqlen)
-    out->parts = m3::delta_in_parts(a->batch * H, out->nc, a->headdim);
-    out->carry = m3::delta_in_parts(a->batch * H, (a->seqlen + m3::kDC - 1) / m3::kDC, a->headdim)
+    out->parts = m3::delta_in_parts(a->batch * H, out->nc, a->headdim, a->io_dtype);
+    out->carry = m3::delta_in_parts(a->batch * H, (a->seqlen + m3::kDC - 1) / m3::kDC, a->headdim, a->io_dtype)
                      ? up256((size_t)(a->batch * H * a->dstate * a->headdim) * 4)
                      : 0;
     out->fwd = n == 0 ? 0 : out->tri_w + out->tri_o + out->sc + out->order + out->carry;

@@ -33,7 +33,7 @@ hipError_t launch_delta_parts(const DeltaParams& p, hipStream_t stream)
     static std::atomic<uint64_t> done{0};
     hipError_t e = delta_allow_lds(kern, lds, done);
     if (e != hipSuccess) return e;
-    const int64_t each = (p.nc + kDeltaParts - 1) / kDeltaParts;
+    const int64_t each = delta_part((int64_t)p.rows * p.H, sizeof(IO) == 4 ? 0 : 1);
     auto part = [&](int64_t from) {
         DeltaParams q = p;
         q.from = from;

@@ -387,9 +387,10 @@ def test_many_short_sequences(rows):
         check_h(hL[at.cuda()], wh, "length %d" % n)
 
 
-@pytest.mark.parametrize("io,N,P,B,H,L", [("f32", 32, 32, 2, 3, 16500), ("bf16", 128, 32, 3, 2, 16384), ("bf16", 64, 64, 1, 2, 16449)])
+@pytest.mark.parametrize("io,N,P,B,H,L", [("f32", 32, 32, 2, 3, 16500), ("bf16", 128, 32, 3, 4, 16384), ("bf16", 64, 64, 1, 10, 16449),
+                                            ("bf16", 64, 128, 1, 20, 6700), ("f32", 128, 64, 1, 17, 4096)])
 def test_long_in_parts(io, N, P, B, H, L):
-    """Rows of 256 chunks and more on few CUs: the walk runs in parts that hand on the state."""
+    """Rows of many chunks on few CUs: the walk runs in parts that hand on the state."""
     say("case parts", io, N, P, B, H, L)
     x = ref.inputs(B, L, H, H, N, P, DT[io], 71)
     h = torch.randn(B, H, N, P, generator=torch.Generator().manual_seed(72)).cuda()
@@ -404,7 +405,7 @@ def test_long_in_parts(io, N, P, B, H, L):
 
 def test_long_packed_in_parts():
     """Rows that end in the first part and in later ones; records in slots, one row without a record, a slot named twice."""
-    N, P, H = 64, 64, 1
+    N, P, H = 64, 64, 2
     lens, slots = [16400, 70, 0, 100, 4200, 16390], [2, 0, 5, 2, 3, -1]
     x = ref.inputs(1, sum(lens), H, H, N, P, torch.bfloat16, 81)
     pool = torch.randn(6, H, N, P, generator=torch.Generator().manual_seed(82)).cuda()
