@@ -424,3 +424,33 @@ def test_long_packed_in_parts():
             check_h(pool[s:s + 1], wh, "row %d" % i)
     for s in (1, 4, 5):
         assert torch.equal(pool[s], before[s])
+
+
+def test_parts_captured_and_on_two_streams():
+    """A call in parts, captured and replayed between eager calls, and two such calls beside each other on streams of their own."""
+    B, L, H, N, P = 1, 16449, 10, 64, 64
+    x = ref.inputs(B, L, H, H, N, P, torch.bfloat16, 91)
+    h = torch.randn(B, H, N, P, generator=torch.Generator().manual_seed(92)).cuda()
+    run = lambda: m3_delta_fwd(*x, h, l2norm=True, scale=0.2)
+    run()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        outs = run()
+    for seed in (93, 94, 95):
+        for dst, src in zip(x, ref.inputs(B, L, H, H, N, P, torch.bfloat16, seed)):
+            dst.copy_(src)
+        want = [t.clone() for t in run()]
+        for t in outs:
+            t.zero_()
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        for a, b in zip(outs, want):
+            assert torch.equal(a, b)
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    got = [m3_delta_fwd(*x, h, l2norm=True, scale=0.2, stream=s) for s in streams]
+    torch.cuda.synchronize()
+    for g in got:
+        for a, b in zip(g, want):
+            assert torch.equal(a, b)
