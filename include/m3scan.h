@@ -438,8 +438,8 @@ int m3_decode_supported(int64_t dstate, int64_t headdim, int64_t rank, int32_t i
  *            first has the record, the others' outputs are NaN.  Slots that no
  *            row names are left as they were.
  * Products run on bf16 matrix cores with float32 operands split into up to
- * three bf16 values and float32 sums: states and gradients have float32's
- * accuracy for both io dtypes.  NaN and Inf inputs propagate as in
+ * three bf16 values and float32 sums: states, outputs and gradients have
+ * float32's accuracy for both io dtypes; a bf16 output is rounded once.  NaN and Inf inputs propagate as in
  * m3_scan_fwd (within their chunk of 64 tokens also to earlier tokens).
  * A workspace holds one call's intermediate values: calls that may run beside
  * each other (streams, replayed graphs) need one each.

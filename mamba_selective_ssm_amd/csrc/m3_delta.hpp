@@ -19,6 +19,9 @@
 // adds the plane products that float32 can still see: 3 where one side is an
 // exact bf16 value, 6 where both have three planes.  At 16x16x32 that is 48
 // and 96 cycles against 256 of the float32 instructions for the same product.
+// Every product's operands are held so, the output's too: a bf16 output is one
+// rounding of a value as exact as float32's (with two planes for S, U and A there
+// its error before that rounding was 2.5e-6 of the outputs' size, for 1e-7 now).
 #pragma once
 
 #include "m3_device.hpp"
@@ -50,7 +53,7 @@ struct DeltaParams {
     float* carry_out;      // and behind it where it is not the last
     // workspace, one entry per (chunk slot, head)
     bf16* tf;              // T in operand order
-    bf16* af;              // scale D o Q K^T in operand order
+    float* af;             // scale D o Q K^T in operand order
     float* sc;             // [kDScal][64] per-token factors
     int* order;            // [rows] packed rows, most chunks first (NULL: as they stand)
 };
@@ -103,12 +106,10 @@ constexpr bool delta_in_parts(int64_t units, int64_t nc, int64_t P, int io_dtype
     return units * (P / 16) <= 192 && nc >= 2 * delta_part(units, io_dtype) && units * nc > 2 * delta_part_size(io_dtype);
 }
 
-// Planes of float32 operands on the state's path and on the output's path, and
-// of the io type's own values.  The output of a bf16 call is rounded to bf16
-// once more, so two planes (16 bits) are enough on its path.
+// Planes of float32 operands, and of the io type's own values.
 template <typename IO> struct DeltaPlanes;
-template <> struct DeltaPlanes<bf16> { static constexpr int io = 1, wide = 3, out = 2; };
-template <> struct DeltaPlanes<float> { static constexpr int io = 3, wide = 3, out = 3; };
+template <> struct DeltaPlanes<bf16> { static constexpr int io = 1, wide = 3; };
+template <> struct DeltaPlanes<float> { static constexpr int io = 3, wide = 3; };
 
 // Row m of 16 x 16 tile i, for the tokens of a chunk and for the rows of the
 // state alike.  A result tile leaves rows 4 g + r (r = 0..3) in lane (l, g);
@@ -122,7 +123,7 @@ __host__ __device__ constexpr int tile_row(int i, int m) { return 32 * (i >> 1) 
 constexpr int kTriBlocks = 6;
 __host__ __device__ constexpr int low_block(int w, int kb) { return w + 2 * kb; }
 
-inline size_t delta_tri_elems(int planes) { return (size_t)kTriBlocks * planes * 512; }
+constexpr size_t kTriValues = (size_t)kTriBlocks * 512;
 
 // What a wavefront's lanes have written to LDS before is there for all its
 // lanes after: its LDS instructions run in order, so only the compiler's order
@@ -271,6 +272,42 @@ __device__ __forceinline__ void mma_planes(const bf16x8 (&a)[PA], const bf16x8 (
 __device__ __forceinline__ bf16x8 join8(const bf16x4& a, const bf16x4& b)
 {
     return __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
+}
+
+// The same in three planes by cutting off after 8 and 16 bits: each plane is the
+// upper half of what those before it left.  More instructions than planes8, of a
+// kind that the state waves beside do not wait for: delta_wide's output waves
+// with planes8 / this: 166 / 157 us (N = 64, P = 96, 96 rows and heads, 2048
+// tokens); delta_walk's, whose time is the way from LDS to the product: 78 / 82
+// (N = P = 64, 64 of them).
+__device__ __forceinline__ void cut8(const f32x4& a, const f32x4& b, bf16x8 (&o)[3])
+{
+    typedef __attribute__((__vector_size__(4 * sizeof(unsigned)))) unsigned u32x4;
+    u32x4 r[3];
+#pragma unroll
+    for (int e = 0; e < 8; e += 2) {
+        float x = e < 4 ? a[e & 3] : b[e & 3], y = e < 4 ? a[(e & 3) + 1] : b[(e & 3) + 1];
+#pragma unroll
+        for (int i = 0; i < 3; ++i) {
+            const unsigned ux = __builtin_bit_cast(unsigned, x), uy = __builtin_bit_cast(unsigned, y);
+            r[i][e / 2] = __builtin_amdgcn_perm(uy, ux, 0x07060302u);
+            if (i < 2) {
+                x -= __builtin_bit_cast(float, ux & 0xffff0000u);
+                y -= __builtin_bit_cast(float, uy & 0xffff0000u);
+            }
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < 3; ++i) o[i] = __builtin_bit_cast(bf16x8, r[i]);
+}
+
+template <int PL> __device__ __forceinline__ void planes8(const f32x4& a, const f32x4& b, bf16x8 (&o)[PL])
+{
+    bf16x4 x[PL], y[PL];
+    to_planes4<PL>(a, x);
+    to_planes4<PL>(b, y);
+#pragma unroll
+    for (int i = 0; i < PL; ++i) o[i] = join8(x[i], y[i]);
 }
 
 __device__ __forceinline__ bf16x8 zero8()

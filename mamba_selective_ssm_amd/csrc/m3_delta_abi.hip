@@ -71,10 +71,11 @@ m3_status plan_delta(const m3_delta_args* a, bool train, DeltaPlan* out)
     out->G = a->ngroups > 0 ? a->ngroups : H;
     out->nc = (longest + m3::kDC - 1) / m3::kDC;
     if (a->batch > 0 && H > 0 && out->nc > kMaxBlocks256 / (a->batch * H)) return M3_ERR_UNSUPPORTED;
-    // the walks: 16 columns of one row and head to a workgroup, 448 threads, or
-    // twice 320; the other kernels that the gradient adds
+    // the walks: 16 columns of one row and head to a workgroup, 512 threads
+    // (bf16: so few in one workgroup only where there are few, else 32 columns,
+    // 448 threads), or twice 320; the other kernels that the gradient adds
     const int64_t slices = (a->batch * H + 7) / 8 * 8 * (a->headdim / 16);
-    if (slices > kMaxThreads / (train ? 640 : 448)) return M3_ERR_UNSUPPORTED;
+    if (slices > kMaxThreads / (train ? 640 : a->io_dtype == M3_F32 ? 512 : 448)) return M3_ERR_UNSUPPORTED;
     if (train) {
         const int64_t tok = packed ? a->seqlen : a->batch * a->seqlen;   // dense: 64 chunks' worth at most
         if (a->batch >= kMaxBlocks256) return M3_ERR_UNSUPPORTED;
@@ -82,10 +83,9 @@ m3_status plan_delta(const m3_delta_args* a, bool train, DeltaPlan* out)
     }
     const int64_t slots = packed ? a->seqlen / m3::kDC + a->batch + 1 : a->batch * out->nc;
     out->chunks = slots * H;
-    const int wide = 3, opl = a->io_dtype == M3_F32 ? 3 : 2;
     const size_t n = (size_t)out->chunks;
-    out->tri_w = up256(n * m3::delta_tri_elems(wide) * 2);
-    out->tri_o = up256(n * m3::delta_tri_elems(opl) * 2);
+    out->tri_w = up256(n * m3::kTriValues * 3 * 2);   // three bf16 planes
+    out->tri_o = up256(n * m3::kTriValues * 4);       // float32
     out->sc = up256(n * m3::kDScal * 64 * 4);
     out->st = up256(n * (size_t)(a->dstate * a->headdim) * 4);
     out->rowsP = up256(n * (size_t)(64 * a->headdim) * 4);
@@ -268,7 +268,7 @@ m3_status m3_delta_fwd(const m3_delta_args* a, void* stream)
     m3::DeltaParams p = params_of(a, pl);
     char* w = static_cast<char*>(a->workspace);
     p.tf = reinterpret_cast<m3::bf16*>(w);
-    p.af = reinterpret_cast<m3::bf16*>(w + pl.tri_w);
+    p.af = reinterpret_cast<float*>(w + pl.tri_w);
     p.sc = reinterpret_cast<float*>(w + pl.tri_w + pl.tri_o);
     if (pl.order > 0 && pl.nc > 0) p.order = reinterpret_cast<int*>(w + pl.tri_w + pl.tri_o + pl.sc);
     if (pl.parts) p.carry_in = p.carry_out = reinterpret_cast<float*>(w + pl.tri_w + pl.tri_o + pl.sc + pl.order);

@@ -42,29 +42,24 @@ __device__ __forceinline__ double wave_inclusive_sum_d(double v)
     return v;
 }
 
-// The operand blocks of a lower triangular matrix in LDS as planes: block (w,
-// kb) has rows tile_row(w, l), columns 32 kb + 8 g ..+7; zero above the diagonal.
-template <int PL, int LD> __device__ __forceinline__ void put_lower(bf16* dst, const float* M, int l, int g, int lane)
+// The operand blocks of a lower triangular matrix in LDS: block (w, kb) has
+// rows tile_row(w, l), columns 32 kb + 8 g ..+7; zero above the diagonal.  f(block,
+// its two halves of 4 columns).
+template <int LD, typename F> __device__ __forceinline__ void each_lower(const float* M, int l, int g, const F& f)
 {
 #pragma unroll
     for (int w = 0; w < 4; ++w)
 #pragma unroll
         for (int kb = 0; kb <= w / 2; ++kb) {
             const int row = tile_row(w, l), c0 = 32 * kb + 8 * g;
-            const f32x4 a = *reinterpret_cast<const f32x4*>(M + row * LD + c0);
-            const f32x4 b = *reinterpret_cast<const f32x4*>(M + row * LD + c0 + 4);
-            bf16x8 o[PL];
+            f32x4 a = *reinterpret_cast<const f32x4*>(M + row * LD + c0);
+            f32x4 b = *reinterpret_cast<const f32x4*>(M + row * LD + c0 + 4);
 #pragma unroll
-            for (int e = 0; e < 8; e += 2) {
-                const float x = e < 4 ? a[e & 3] : b[e & 3], y = e < 4 ? a[(e & 3) + 1] : b[(e & 3) + 1];
-                bf16x2 t[PL];
-                to_planes2<PL>(c0 + e <= row ? x : 0.f, c0 + e + 1 <= row ? y : 0.f, t);
-#pragma unroll
-                for (int i = 0; i < PL; ++i) { o[i][e] = t[i][0]; o[i][e + 1] = t[i][1]; }
+            for (int e = 0; e < 4; ++e) {
+                a[e] = c0 + e <= row ? a[e] : 0.f;
+                b[e] = c0 + 4 + e <= row ? b[e] : 0.f;
             }
-#pragma unroll
-            for (int i = 0; i < PL; ++i)
-                *reinterpret_cast<bf16x8*>(dst + (low_block(w, kb) * PL + i) * 512 + lane * 8) = o[i];
+            f(low_block(w, kb), a, b);
         }
 }
 
@@ -98,7 +93,7 @@ constexpr int kChunkLds = (64 * 68 + 5 * 64) * 4;   // bytes
 template <typename IO, int N, bool BWD>
 __device__ __forceinline__ void delta_chunk(const DeltaParams& p, int64_t bid, char* lds)
 {
-    constexpr int KP = DeltaPlanes<IO>::io, WP = DeltaPlanes<IO>::wide, OP = DeltaPlanes<IO>::out;
+    constexpr int KP = DeltaPlanes<IO>::io, WP = DeltaPlanes<IO>::wide;
     constexpr int KB = N / 32, LD = 68;
     float* sM = reinterpret_cast<float*>(lds);
     float *sGh = sM + 64 * LD, *sGl = sGh + 64, *sBk = sGl + 64, *sRk = sBk + 64, *sRq = sRk + 64;
@@ -252,7 +247,11 @@ __device__ __forceinline__ void delta_chunk(const DeltaParams& p, int64_t bid, c
         } else {
             wave_order();
             sc[192] = p.scale * eG * sRq[lane];
-            put_lower<OP, LD>(p.af + ci * (kTriBlocks * OP * 512), sM, l, g, lane);
+            float* dst = p.af + ci * (int64_t)kTriValues + 4 * lane;
+            each_lower<LD>(sM, l, g, [&](int i, const f32x4& a, const f32x4& b) {
+                *reinterpret_cast<f32x4*>(dst + 512 * i) = a;
+                *reinterpret_cast<f32x4*>(dst + 512 * i + 256) = b;
+            });
         }
     }
 
@@ -331,7 +330,13 @@ __device__ __forceinline__ void delta_chunk(const DeltaParams& p, int64_t bid, c
             for (int tb = 0; tb < 2; ++tb) tile_put<LD>(&sM[(32 + 16 * ta) * LD + 16 * tb], l, g, -x[ta][tb]);
     }
     wave_order();
-    put_lower<WP, LD>(p.tf + ci * (kTriBlocks * WP * 512), sM, l, g, lane);
+    bf16* dst = p.tf + ci * (int64_t)(kTriValues * WP) + 8 * lane;
+    each_lower<LD>(sM, l, g, [&](int i, const f32x4& a, const f32x4& b) {
+        bf16x8 o[WP];
+        planes8<WP>(a, b, o);
+#pragma unroll
+        for (int j = 0; j < WP; ++j) *reinterpret_cast<bf16x8*>(dst + (i * WP + j) * 512) = o[j];
+    });
 }
 
 template <typename IO, int N, bool BWD>

@@ -10,7 +10,7 @@ namespace {
 // workgroups [0, walks) have the walk, each wavefront of the others a chunk and
 // head.  The walk alone leaves the CUs idle that it has no slices for.
 template <typename IO, int N>
-__global__ __launch_bounds__(64 * 7) void delta_both_kernel(const DeltaParams p, const DeltaParams next, const unsigned walks)
+__global__ __launch_bounds__(64 * 8) void delta_both_kernel(const DeltaParams p, const DeltaParams next, const unsigned walks)
 {
     extern __shared__ __attribute__((aligned(16))) char wlds[];
     if (blockIdx.x < walks) {
@@ -18,7 +18,7 @@ __global__ __launch_bounds__(64 * 7) void delta_both_kernel(const DeltaParams p,
         return;
     }
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int64_t unit = (int64_t)(blockIdx.x - walks) * 7 + wave;
+    const int64_t unit = (int64_t)(blockIdx.x - walks) * 8 + wave;
     if (unit < (int64_t)next.rows * next.nc * next.H) delta_chunk<IO, N, false>(next, unit, wlds + wave * kChunkLds);
 }
 
@@ -26,8 +26,8 @@ template <typename IO, int N>
 hipError_t launch_delta_parts(const DeltaParams& p, hipStream_t stream)
 {
     using Cf = WalkCfg<IO, N, false>;
-    static_assert(Cf::waves == 7, "a wavefront to each of delta_both_kernel's chunks");
-    constexpr size_t lds = Cf::total > 7 * kChunkLds ? Cf::total : 7 * kChunkLds;
+    static_assert(Cf::waves == 8, "a wavefront to each of delta_both_kernel's chunks");
+    constexpr size_t lds = Cf::total > 8 * kChunkLds ? Cf::total : 8 * kChunkLds;
     static_assert(lds <= 160 * 1024, "a workgroup's LDS");
     auto* const kern = &delta_both_kernel<IO, N>;
     static std::atomic<uint64_t> done{0};
@@ -50,8 +50,8 @@ hipError_t launch_delta_parts(const DeltaParams& p, hipStream_t stream)
         DeltaParams next = now;
         next.nc = 0;
         if (c + each < p.nc) next = part(c + each);
-        const unsigned chunks = (unsigned)(((int64_t)p.rows * next.nc * p.H + 6) / 7);
-        hipLaunchKernelGGL(kern, dim3(walks + chunks), dim3(64 * 7), lds, stream, now, next, walks);
+        const unsigned chunks = (unsigned)(((int64_t)p.rows * next.nc * p.H + 7) / 8);
+        hipLaunchKernelGGL(kern, dim3(walks + chunks), dim3(64 * 8), lds, stream, now, next, walks);
         if ((e = hipGetLastError()) != hipSuccess) return e;
     }
     return hipSuccess;

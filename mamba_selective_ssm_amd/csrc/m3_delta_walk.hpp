@@ -21,8 +21,15 @@ namespace m3 {
 //     LDS, NBUF - 1 chunks ahead (float32 K through its registers, where it is
 //     split into planes: read two chunks ahead, 29 us for 37 at 32 slices of 13
 //     chunks, N = 64);
-//   - two output wavefronts make O from the S and U planes, Q S
-//     while the state goes through T, A U during the next chunk's first stage.
+//   - three output wavefronts make O from the planes of S and from U, Q S
+//     while the state goes through T, A U during the next chunk's first stage:
+//     row tiles 0 and 1, tile 2, and tile 3, which A spans with two blocks each.
+//     A and U come as float32 and are split into planes here, half of A beside
+//     each of the later stages, where these wavefronts have the least to do (all
+//     of A beside one of them: 2 us more at 256 slices of N = 64, below, or 10
+//     to 40 us at 128 slices of 1024 chunks, N = 128).  With two wavefronts, row
+//     tiles 0, 1 and 2, 3, the splits held up the state's: 83 for 78 us a call at
+//     256 slices, 1990 for 1935 at 128.
 // Three buffers (two chunks ahead) for the forward bf16 walk: with two the 256
 // slices below take 5 us more, N = 128 over 65536 tokens 2098 -> 2503 us.
 //
@@ -40,19 +47,19 @@ namespace m3 {
 // on a CU: 90 us for both walks at 256 slices each (N = P = 64, 32 chunks), 102
 // to 113 us with two chunks ahead and one workgroup to a CU.
 template <typename IO, int N, bool TRAIN> struct WalkCfg {
-    static constexpr int KP = DeltaPlanes<IO>::io, WP = DeltaPlanes<IO>::wide, OP = DeltaPlanes<IO>::out;
+    static constexpr int KP = DeltaPlanes<IO>::io, WP = DeltaPlanes<IO>::wide;
     static constexpr bool DIRECT = KP == 1;           // io values are operands as they are: loads go straight to LDS
     static constexpr int NBUF = DIRECT && !TRAIN ? 3 : 2;
     static constexpr int KB = N / 32, NT = N / 16, TI = (NT + 3) / 4;
-    static constexpr int outs = TRAIN ? 0 : 2, waves = 4 + outs + 1;
+    static constexpr int outs = TRAIN ? 0 : 3, waves = 4 + outs + 1;
     // bytes of one buffer (T apart: the gradient has one, and float32 at N = 128,
     // whose planes leave room for one)
     static constexpr int k = 0, f = k + KP * 64 * N * 2, v = f + 5 * 256, buf = v + (DIRECT ? 64 * 32 : 0);
     static constexpr int tsize = kTriBlocks * WP * 1024, TB = TRAIN || (!DIRECT && N == 128) ? 1 : NBUF;
     static constexpr int t = NBUF * buf;
-    // then the planes of S, R, d U, U, and the rows of O
+    // then the planes of S, R, d U, U itself, and the rows of O
     static constexpr int ex = t + TB * tsize, s = 0, r = s + WP * KB * 1024, u2 = r + WP * 2048, u = u2 + WP * 2048,
-                         o = u + OP * 2048, total = ex + (TRAIN ? u : o + 64 * 16 * (int)sizeof(IO));
+                         o = u + 4096, total = ex + (TRAIN ? u : o + 64 * 16 * (int)sizeof(IO));
     // loads of one chunk by the loader (DIRECT): T, factors, K, V
     static constexpr int loads = kTriBlocks * WP + 2 + 64 * N * 2 / 1024 + 2;
 };
@@ -232,7 +239,7 @@ template <typename IO, int N, bool TRAIN>
 __device__ __forceinline__ void delta_walk(const DeltaParams& p, float* Sbuf, float* Ubuf, int64_t bid, char* wlds)
 {
     using Cf = WalkCfg<IO, N, TRAIN>;
-    constexpr int KP = Cf::KP, WP = Cf::WP, OP = Cf::OP, KB = Cf::KB, NT = Cf::NT, TI = Cf::TI, NBUF = Cf::NBUF;
+    constexpr int KP = Cf::KP, WP = Cf::WP, KB = Cf::KB, NT = Cf::NT, TI = Cf::TI, NBUF = Cf::NBUF;
 
     const int tid = threadIdx.x, lane = tid & 63, l = lane & 15, g = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -262,117 +269,120 @@ __device__ __forceinline__ void delta_walk(const DeltaParams& p, float* Sbuf, fl
     char* ex = wlds + Cf::ex + 16 * lane;
 
     if constexpr (!TRAIN)
-    if (wave >= 4) {   // output: row tiles 2 o, 2 o + 1
+    if (wave >= 4) {   // output: row tiles 0 and 1, tile 2, tile 3, two of A's blocks each
         // No load depends on a branch: where one might, a wait for the chunk's
         // operands would also wait for those of the chunk after it.
-        auto output = [&](auto half_) {
-        constexpr int o = decltype(half_)::value;
+        auto output = [&](auto first_) {
+        constexpr bool FIRST = decltype(first_)::value;
+        constexpr int TO = FIRST ? 2 : 1;            // row tiles
+        const int tile = FIRST ? 0 : wave - 3;       // the first
         const IO* qp = reinterpret_cast<const IO*>(p.q) + (row.start * p.G + h / (p.H / p.G)) * N + 8 * g;
         IO* op = reinterpret_cast<IO*>(p.o) + (row.start * p.H + h) * p.P + p0;
-        IO* so = reinterpret_cast<IO*>(wlds + Cf::ex + Cf::o) + 32 * o * 16;   // this wave's rows
-        RawRow8<IO> q[2][KB];
-        struct Tri {
-            bf16x8 a0[2][OP], a1[2][OP];
-        } ta, tb;
-        f32x4 acc[2] = {fz, fz}, out[2];
+        IO* so = reinterpret_cast<IO*>(wlds + Cf::ex + Cf::o) + (FIRST ? 0 : 16 * tile) * 16;   // this wave's rows, tile by tile
+        RawRow8<IO> q[TO][KB];
+        f32x4 a[2][2];   // [block][half]
+        bf16x8 a8[2][WP], u8[2][WP];
+        f32x4 acc[TO], out[TO];
         auto load = [&](int c) {
             c = c < nch ? c : nch - 1;
             const int end = c == nch - 1 ? nlast - 1 : kDC - 1;
             const IO* qc = qp + (int64_t)c * kDC * rs;
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const int t = tile_row(2 * o + i, l) < end ? tile_row(2 * o + i, l) : end;
+            for (int i = 0; i < TO; ++i) {
+                const int t = tile_row(tile + i, l) < end ? tile_row(tile + i, l) : end;
 #pragma unroll
                 for (int kb = 0; kb < KB; ++kb) q[i][kb].load(qc + t * rs + 32 * kb, true);
             }
         };
-        auto load_a = [&](Tri& x, int c) {   // blocks (2 o + i, 0), and (2 + i, 1) of the lower tiles
+        auto load_a = [&](int c) {   // blocks (0, 0) and (1, 0), or (tile, 0) and (tile, 1)
             c = c < nch ? c : nch - 1;
-            const bf16* src = p.af + (ci0 + (int64_t)c * p.H) * (kTriBlocks * OP * 512) + lane * 8;
+            const float* src = p.af + (ci0 + (int64_t)c * p.H) * (int64_t)kTriValues + 4 * lane;
 #pragma unroll
             for (int i = 0; i < 2; ++i)
 #pragma unroll
-                for (int j = 0; j < OP; ++j) x.a0[i][j] = *reinterpret_cast<const bf16x8*>(src + ((2 * o + i) * OP + j) * 512);
-            if (o)
-#pragma unroll
-                for (int i = 0; i < 2; ++i)
-#pragma unroll
-                    for (int j = 0; j < OP; ++j) x.a1[i][j] = *reinterpret_cast<const bf16x8*>(src + ((4 + i) * OP + j) * 512);
+                for (int j = 0; j < 2; ++j)
+                    a[i][j] = *reinterpret_cast<const f32x4*>(src + (FIRST ? low_block(i, 0) : low_block(tile, i)) * 512 + 256 * j);
         };
-        auto add_u = [&](const Tri& x) {   // + A U
+        auto split_a = [&](int i) { planes8<WP>(a[i][0], a[i][1], a8[i]); };
+        auto split_u = [&]() {
 #pragma unroll
-            for (int i = 0; i < 2; ++i) out[i] = acc[i];
-            bf16x8 u8[2][OP];
+            for (int kb = 0; kb < (FIRST ? 1 : 2); ++kb)
+                planes8<WP>(*reinterpret_cast<const f32x4*>(ex + Cf::u + 2 * kb * 1024),
+                            *reinterpret_cast<const f32x4*>(ex + Cf::u + (2 * kb + 1) * 1024), u8[kb]);
+        };
+        auto add_u = [&]() {   // + A U
 #pragma unroll
-            for (int kb = 0; kb < 2; ++kb)
-#pragma unroll
-                for (int j = 0; j < OP; ++j) u8[kb][j] = *reinterpret_cast<const bf16x8*>(ex + Cf::u + (2 * j + kb) * 1024);
-            mma_tiles<2, OP, OP, OP>(x.a0, u8[0], out);
-            if (o) mma_tiles<2, OP, OP, OP>(x.a1, u8[1], out);
+            for (int i = 0; i < TO; ++i) out[i] = acc[i];
+            if constexpr (FIRST) {
+                mma_tiles<2, WP, WP, WP>(a8, u8[0], out);
+            } else {
+                mma_planes<WP, WP, WP>(a8[0], u8[0], out[0]);
+                mma_planes<WP, WP, WP>(a8[1], u8[1], out[0]);
+            }
         };
         auto store = [&](int c) {   // through LDS: 16 bytes of a row to a lane, not 2
 #pragma unroll
-            for (int i = 0; i < 2; ++i)
+            for (int i = 0; i < TO; ++i)
 #pragma unroll
-                for (int r = 0; r < 4; ++r) so[(8 * g + 4 * i + r) * 16 + l] = from_f32<IO>(out[i][r]);
+                for (int r = 0; r < 4; ++r) so[(16 * i + 4 * g + r) * 16 + l] = from_f32<IO>(out[i][r]);
             wave_order();
             const int nv = c == nch - 1 ? nlast : kDC;
             IO* oc = op + (int64_t)c * kDC * vs;
-            constexpr int per = 16 / sizeof(IO), lpr = 16 / per;   // values to a lane, lanes to a row
+            constexpr int per = 16 / sizeof(IO), lpr = 16 / per, rows = 64 / lpr;   // values to a lane, lanes to a row, rows to a store
 #pragma unroll
-            for (int i = 0; i < lpr / 2; ++i) {
-                const int t = (64 / lpr) * i + lane / lpr, j = lane % lpr;
-                const uint4 x = *reinterpret_cast<const uint4*>(so + t * 16 + per * j);
-                if (32 * o + t < nv) *reinterpret_cast<uint4*>(oc + (32 * o + t) * vs + per * j) = x;
+            for (int i = 0; i < (16 * TO + rows - 1) / rows; ++i) {
+                const int m = rows * i + lane / lpr, j = lane % lpr;
+                const int t = tile_row(tile + (m >> 4), m & 15);
+                if (m < 16 * TO && t < nv)
+                    *reinterpret_cast<uint4*>(oc + t * vs + per * j) = *reinterpret_cast<const uint4*>(so + m * 16 + per * j);
             }
             wave_order();
         };
         if (nch > 0) {
             load(0);
-            load_a(ta, 0);
-            load_a(tb, 0);
+            load_a(0);
         }
         __syncthreads();
-        auto step = [&](Tri& cur, Tri& prev, int c) {
-            add_u(prev);   // (the first chunk's goes nowhere)
+        for (int c = 0; c < nch; ++c) {
+            if (c > 0) {
+                add_u();
+                store(c - 1);
+            }
             __syncthreads();   // R
-            acc[0] = fz;
-            acc[1] = fz;
-            f32x4 fo[2];
 #pragma unroll
-            for (int i = 0; i < 2; ++i)
-                fo[i] = *reinterpret_cast<const f32x4*>(wlds + (c % NBUF) * Cf::buf + Cf::f + 4 * (192 + 32 * o + 8 * g + 4 * i));
+            for (int i = 0; i < TO; ++i) acc[i] = fz;
+            f32x4 fo[TO];
+#pragma unroll
+            for (int i = 0; i < TO; ++i)
+                fo[i] = *reinterpret_cast<const f32x4*>(wlds + (c % NBUF) * Cf::buf + Cf::f + 4 * (192 + tile_row(tile + i, 4 * g)));
+            split_a(0);
 #pragma unroll
             for (int kb = 0; kb < KB; ++kb) {
-                bf16x8 s8[OP], q8[2][KP];
+                bf16x8 s8[WP], q8[TO][KP];
 #pragma unroll
-                for (int j = 0; j < OP; ++j) s8[j] = *reinterpret_cast<const bf16x8*>(ex + Cf::s + (j * KB + kb) * 1024);
+                for (int j = 0; j < WP; ++j) s8[j] = *reinterpret_cast<const bf16x8*>(ex + Cf::s + (j * KB + kb) * 1024);
 #pragma unroll
-                for (int i = 0; i < 2; ++i) q[i][kb].planes(q8[i]);
-                mma_tiles<2, KP, OP, OP>(q8, s8, acc);
+                for (int i = 0; i < TO; ++i) q[i][kb].planes(q8[i]);
+                mma_tiles<TO, KP, WP, WP>(q8, s8, acc);
             }
 #pragma unroll
-            for (int i = 0; i < 2; ++i)
+            for (int i = 0; i < TO; ++i)
 #pragma unroll
                 for (int r = 0; r < 4; ++r) acc[i][r] *= fo[i][r];
             load(c + 1);
             __syncthreads();   // U
-            load_a(prev, c + 1);
-            if (c > 0) store(c - 1);
+            split_u();
+            split_a(1);
+            load_a(c + 1);
             __syncthreads();   // S
-        };
-        for (int c = 0; c < nch; c += 2) {
-            step(ta, tb, c);
-            if (c + 1 < nch) step(tb, ta, c + 1);
         }
         if (nch > 0) {
-            if (nch & 1) add_u(ta);
-            else add_u(tb);
+            add_u();
             store(nch - 1);
         }
         };
-        if (wave & 1) output(std::integral_constant<int, 1>());
-        else output(std::integral_constant<int, 0>());
+        if (wave == 4) output(std::true_type());
+        else output(std::false_type());
         return;
     }
 
@@ -510,11 +520,8 @@ __device__ __forceinline__ void delta_walk(const DeltaParams& p, float* Sbuf, fl
             to_planes4<WP>(u2, o);
 #pragma unroll
             for (int j = 0; j < WP; ++j) *reinterpret_cast<bf16x4*>(ex + Cf::u2 + (2 * j + (w >> 1)) * 1024 + half) = o[j];
-            if (!TRAIN) {
-                bf16x4 q[OP];
-                to_planes4<OP>(U, q);
-#pragma unroll
-                for (int j = 0; j < OP; ++j) *reinterpret_cast<bf16x4*>(ex + Cf::u + (2 * j + (w >> 1)) * 1024 + half) = q[j];
+            if constexpr (!TRAIN) {
+                *reinterpret_cast<f32x4*>(ex + Cf::u + w * 1024) = U;
             } else {
 #pragma unroll
                 for (int r = 0; r < 4; ++r) Ubuf[(ci * 64 + tr0 + r) * p.P + col] = U[r];
@@ -555,7 +562,7 @@ __device__ __forceinline__ void delta_walk(const DeltaParams& p, float* Sbuf, fl
 }
 
 template <typename IO, int N>
-__global__ __launch_bounds__(64 * 7) void delta_walk_kernel(const DeltaParams p)
+__global__ __launch_bounds__(64 * 8) void delta_walk_kernel(const DeltaParams p)
 {
     extern __shared__ __attribute__((aligned(16))) char wlds[];
     delta_walk<IO, N, false>(p, nullptr, nullptr, blockIdx.x, wlds);

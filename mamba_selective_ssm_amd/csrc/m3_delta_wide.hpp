@@ -13,7 +13,7 @@ namespace m3 {
 // the products.  A step takes it longer than four wavefronts together (four
 // times their products), but it reads a quarter of what they read from LDS,
 // which is what bounds a CU that runs several of them, and one K, T and set of
-// factors serves NS of them.  The state waves leave the planes of S and U for
+// factors serves NS of them.  The state waves leave S and U for
 // four output waves, each with two row tiles of half the column groups (all
 // groups of one tile read twice as much LDS, and buffers twice as large left no
 // room for NS = 4 at N = 128: 508 for 375 us there, below); Q S beside R and U,
@@ -25,18 +25,25 @@ namespace m3 {
 // 5 us a chunk and CU: matrix cores busy for 33% of them, vector units 31%, LDS
 // 31% and 10% in bank conflicts, the chain's waits the rest.
 template <int N, int NS> struct WideCfg {
-    static constexpr int WP = DeltaPlanes<bf16>::wide, OP = DeltaPlanes<bf16>::out;
+    static constexpr int WP = DeltaPlanes<bf16>::wide;
     static constexpr int KB = N / 32, NT = N / 16, waves = NS + 5;
-    // bytes of one of two buffers, then per column group the planes of S and U
+    // S and U go to the output waves as planes, so that they need not split what
+    // the state waves have split, or as float32, where planes would leave room for
+    // one workgroup on a CU instead of two.  Calls over 2048 tokens, us, planes /
+    // float32: NS = 4: 128 rows and heads at N = P = 128: 187 / 205, 256 at N =
+    // 128, P = 64: 285 / 307; NS = 2: 96 at N = 64, P = 96: 180 / 157, 192: 290 /
+    // 275.
+    static constexpr bool PLANES = NS == 4;
+    // bytes of one of two buffers, then per column group S and U
     static constexpr int k = 0, t = k + 64 * N * 2, f = t + kTriBlocks * WP * 1024, v = f + 5 * 256, buf = v + 64 * NS * 32;
-    static constexpr int ex = 2 * buf, u = OP * KB * 1024, ex1 = u + OP * 2048, total = ex + NS * ex1;
+    static constexpr int ex = 2 * buf, u = PLANES ? WP * KB * 1024 : KB * 2048, ex1 = u + (PLANES ? WP * 2048 : 4096), total = ex + NS * ex1;
 };
 
 template <int N, int NS>
 __global__ __launch_bounds__(64 * (NS + 5)) void delta_wide_kernel(const DeltaParams p)
 {
     using Cf = WideCfg<N, NS>;
-    constexpr int WP = Cf::WP, OP = Cf::OP, KB = Cf::KB, NT = Cf::NT;
+    constexpr int WP = Cf::WP, KB = Cf::KB, NT = Cf::NT;
     extern __shared__ __attribute__((aligned(16))) char wlds[];
 
     const int tid = threadIdx.x, lane = tid & 63, l = lane & 15, g = lane >> 4;
@@ -112,7 +119,8 @@ __global__ __launch_bounds__(64 * (NS + 5)) void delta_wide_kernel(const DeltaPa
         const int t[2] = {tile_row(tile[0], l), tile_row(tile[1], l)};   // this lane's tokens
         const bf16* qp = reinterpret_cast<const bf16*>(p.q) + (row.start * p.G + h / (p.H / p.G)) * N + 8 * g;
         bf16* op = reinterpret_cast<bf16*>(p.o) + (row.start * p.H + h) * p.P + p0 + 16 * cg0 + 4 * g;
-        bf16x8 q[2][KB][1], a[3][OP];
+        bf16x8 q[2][KB][1];
+        f32x4 a[3][2];   // [block][half]
         float fo[2];
         // (No load depends on a branch: where one might, a wait for the chunk's
         // operands would also wait for those of the chunk after it.)
@@ -129,12 +137,21 @@ __global__ __launch_bounds__(64 * (NS + 5)) void delta_wide_kernel(const DeltaPa
         };
         auto load_a = [&](int c) {
             c = c < nch ? c : nch - 1;
-            const bf16* src = p.af + (ci0 + (int64_t)c * p.H) * (kTriBlocks * OP * 512) + lane * 8;
+            const float* src = p.af + (ci0 + (int64_t)c * p.H) * (int64_t)kTriValues + 4 * lane;
 #pragma unroll
-            for (int j = 0; j < OP; ++j) {
-                a[0][j] = *reinterpret_cast<const bf16x8*>(src + (low_block(tile[0], 0) * OP + j) * 512);
-                a[1][j] = *reinterpret_cast<const bf16x8*>(src + (low_block(tile[1], 0) * OP + j) * 512);
-                a[2][j] = *reinterpret_cast<const bf16x8*>(src + (low_block(tile[1], 1) * OP + j) * 512);
+            for (int j = 0; j < 2; ++j) {
+                a[0][j] = *reinterpret_cast<const f32x4*>(src + low_block(tile[0], 0) * 512 + 256 * j);
+                a[1][j] = *reinterpret_cast<const f32x4*>(src + low_block(tile[1], 0) * 512 + 256 * j);
+                a[2][j] = *reinterpret_cast<const f32x4*>(src + low_block(tile[1], 1) * 512 + 256 * j);
+            }
+        };
+        // block kb of the `blocks` of S or U at s
+        auto get = [&](const char* s, int kb, int blocks, bf16x8 (&x)[WP]) {
+            if constexpr (Cf::PLANES) {
+#pragma unroll
+                for (int j = 0; j < WP; ++j) x[j] = *reinterpret_cast<const bf16x8*>(s + (j * blocks + kb) * 1024);
+            } else {
+                cut8(*reinterpret_cast<const f32x4*>(s + kb * 2048), *reinterpret_cast<const f32x4*>(s + kb * 2048 + 1024), x);
             }
         };
         if (nch > 0) {
@@ -151,11 +168,10 @@ __global__ __launch_bounds__(64 * (NS + 5)) void delta_wide_kernel(const DeltaPa
                 acc[1][i] = fz;
 #pragma unroll
                 for (int kb = 0; kb < KB; ++kb) {
-                    bf16x8 s8[1][OP];
+                    bf16x8 s8[1][WP];
+                    get(ex + i * Cf::ex1, kb, KB, s8[0]);
 #pragma unroll
-                    for (int j = 0; j < OP; ++j) s8[0][j] = *reinterpret_cast<const bf16x8*>(ex + i * Cf::ex1 + (j * KB + kb) * 1024);
-#pragma unroll
-                    for (int k = 0; k < 2; ++k) mma_tiles<1, OP, 1, OP>(s8, q[k][kb], &acc[k][i]);
+                    for (int k = 0; k < 2; ++k) mma_tiles<1, WP, 1, WP>(s8, q[k][kb], &acc[k][i]);
                 }
 #pragma unroll
                 for (int k = 0; k < 2; ++k)
@@ -163,16 +179,18 @@ __global__ __launch_bounds__(64 * (NS + 5)) void delta_wide_kernel(const DeltaPa
                     for (int r = 0; r < 4; ++r) acc[k][i][r] *= fo[k];
             }
             load_q(c + 1);
+            bf16x8 a8[3][WP];
+#pragma unroll
+            for (int i = 0; i < 3; ++i) cut8(a[i][0], a[i][1], a8[i]);
             bar();   // U
 #pragma unroll
             for (int i = 0; i < NG; ++i)
 #pragma unroll
                 for (int kb = 0; kb < 2; ++kb) {
-                    bf16x8 u8[1][OP];
-#pragma unroll
-                    for (int j = 0; j < OP; ++j) u8[0][j] = *reinterpret_cast<const bf16x8*>(ex + i * Cf::ex1 + Cf::u + (2 * j + kb) * 1024);
-                    if (kb == 0) mma_tiles<1, OP, OP, OP>(u8, a[0], &acc[0][i]);
-                    mma_tiles<1, OP, OP, OP>(u8, a[1 + kb], &acc[1][i]);
+                    bf16x8 u8[1][WP];
+                    get(ex + i * Cf::ex1 + Cf::u, kb, 2, u8[0]);
+                    if (kb == 0) mma_tiles<1, WP, WP, WP>(u8, a8[0], &acc[0][i]);
+                    mma_tiles<1, WP, WP, WP>(u8, a8[1 + kb], &acc[1][i]);
                 }
             load_a(c + 1);
 #pragma unroll
@@ -201,21 +219,19 @@ __global__ __launch_bounds__(64 * (NS + 5)) void delta_wide_kernel(const DeltaPa
             S[i][r] = hin != nullptr ? hin[(32 * (i >> 1) + 4 * (i & 1) + r) * p.P] : 0.f;
             if (rec == -2) S[i][r] = __builtin_nanf("");   // the record belongs to an earlier row
         }
-    auto planes_of = [&](const f32x4& x, const f32x4& y, bf16x8 (&o)[WP]) {
-        bf16x4 lo[WP], hi[WP];
-        to_planes4<WP>(x, lo);
-        to_planes4<WP>(y, hi);
-#pragma unroll
-        for (int j = 0; j < WP; ++j) o[j] = join8(lo[j], hi[j]);
-    };
     bf16x8 s8[KB][WP];
 #pragma unroll
-    for (int kb = 0; kb < KB; ++kb) planes_of(S[2 * kb], S[2 * kb + 1], s8[kb]);
+    for (int kb = 0; kb < KB; ++kb) planes8<WP>(S[2 * kb], S[2 * kb + 1], s8[kb]);
     auto put_state = [&]() {
+        if constexpr (Cf::PLANES) {
 #pragma unroll
-        for (int kb = 0; kb < KB; ++kb)
+            for (int kb = 0; kb < KB; ++kb)
 #pragma unroll
-            for (int j = 0; j < OP; ++j) *reinterpret_cast<bf16x8*>(ex + (j * KB + kb) * 1024) = s8[kb][j];
+                for (int j = 0; j < WP; ++j) *reinterpret_cast<bf16x8*>(ex + (j * KB + kb) * 1024) = s8[kb][j];
+        } else {
+#pragma unroll
+            for (int i = 0; i < NT; ++i) *reinterpret_cast<f32x4*>(ex + i * 1024) = S[i];
+        }
     };
     put_state();
     bar();
@@ -245,8 +261,8 @@ __global__ __launch_bounds__(64 * (NS + 5)) void delta_wide_kernel(const DeltaPa
 #pragma unroll
             for (int r = 0; r < 4; ++r) P[rt][r] = fb[r] * (float)v[r] - fp[r] * P[rt][r];
         }
-        planes_of(P[0], P[1], r8[0]);
-        planes_of(P[2], P[3], r8[1]);
+        planes8<WP>(P[0], P[1], r8[0]);
+        planes8<WP>(P[2], P[3], r8[1]);
         // U = T R
         f32x4 U[4] = {fz, fz, fz, fz};
         {
@@ -263,13 +279,17 @@ __global__ __launch_bounds__(64 * (NS + 5)) void delta_wide_kernel(const DeltaPa
                 for (int j = 0; j < WP; ++j) t2[i][j] = *reinterpret_cast<const bf16x8*>(tb + ((4 + i) * WP + j) * 1024);
             mma_tiles<2, WP, WP, WP>(t2, r8[1], U + 2);
         }
+        if constexpr (Cf::PLANES) {
 #pragma unroll
-        for (int kb = 0; kb < 2; ++kb) {
-            bf16x4 lo[OP], hi[OP];
-            to_planes4<OP>(U[2 * kb], lo);
-            to_planes4<OP>(U[2 * kb + 1], hi);
+            for (int kb = 0; kb < 2; ++kb) {
+                bf16x8 o[WP];
+                planes8<WP>(U[2 * kb], U[2 * kb + 1], o);
 #pragma unroll
-            for (int j = 0; j < OP; ++j) *reinterpret_cast<bf16x8*>(ex + Cf::u + (2 * j + kb) * 1024) = join8(lo[j], hi[j]);
+                for (int j = 0; j < WP; ++j) *reinterpret_cast<bf16x8*>(ex + Cf::u + (2 * j + kb) * 1024) = o[j];
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) *reinterpret_cast<f32x4*>(ex + Cf::u + i * 1024) = U[i];
         }
 #pragma unroll
         for (int rt = 0; rt < 4; ++rt) {
@@ -277,8 +297,8 @@ __global__ __launch_bounds__(64 * (NS + 5)) void delta_wide_kernel(const DeltaPa
 #pragma unroll
             for (int r = 0; r < 4; ++r) U[rt][r] *= fu[r];
         }
-        planes_of(U[0], U[1], r8[0]);
-        planes_of(U[2], U[3], r8[1]);
+        planes8<WP>(U[0], U[1], r8[0]);
+        planes8<WP>(U[2], U[3], r8[1]);
         bar();   // U
         // S <- e^G_last S + K^T (d U)
         const float eL = *reinterpret_cast<const float*>(buf + Cf::f + 1024 + 4 * lane);
@@ -308,7 +328,7 @@ __global__ __launch_bounds__(64 * (NS + 5)) void delta_wide_kernel(const DeltaPa
                     S[i0 + i][r] = eL * S[i0 + i][r] + acc[i][r];
                     S[i0 + i + 1][r] = eL * S[i0 + i + 1][r] + acc[i + 1][r];
                 }
-                planes_of(S[i0 + i], S[i0 + i + 1], s8[(i0 + i) / 2]);
+                planes8<WP>(S[i0 + i], S[i0 + i + 1], s8[(i0 + i) / 2]);
             }
         }
         put_state();
