@@ -1,5 +1,5 @@
-"""How exact the gated delta rule's results are: states, float32 outputs, and
-bf16 outputs before their one rounding.
+"""How exact the gated delta rule's results are: states, float32 outputs,
+gradients, and bf16 outputs before their one rounding.
 
 Bounds.  A rounding to float32 is off by at most 2^-24 of the value, by
 2^-24 / sqrt(3) in the mean square.  A sum of n terms of either sign is rounded
@@ -9,7 +9,9 @@ most N + 2 * 64 = 256 terms: 6.6 * 2^-24 each.  A state or an output has three
 such products behind it, one after the other (K S, T R, K^T U; a float32
 operand's 24 bits add 2^-24 / sqrt(3) a value, and the four factors of decays and
 norms 2^-23 each, which changes nothing): sqrt(3 * 6.6^2 + 4 * 4) * 2^-24 =
-12.1 * 2^-24 = 7.2e-7, asked for below as 2^-20.  It is relative to the 2-norm.
+12.1 * 2^-24 = 7.2e-7, asked for below as 2^-20.  A gradient has six: 2^-20
+sqrt(2).  Both are relative to the 2-norm, for results that are not far smaller
+than their terms.
 
 A bf16 output is one rounding of such a value y.  It differs from the rounding
 of the exact value only where a boundary lies between the two: for an error d and
@@ -25,6 +27,8 @@ The first tests show on the CPU what these bounds see: the chunked form with
 every product's operands held as sums of bf16 values, three of them or, in one
 product at a time, two.
 """
+import math
+
 import pytest
 import torch
 
@@ -32,7 +36,9 @@ import delta_reference as ref
 from helpers import say
 
 ACC = 2.0 ** -20
+GRAD_ACC = ACC * math.sqrt(2.0)
 DT = {"bf16": torch.bfloat16, "f32": torch.float32}
+NAMES = ("dq", "dk", "dv", "dg", "dbeta", "dh_in")
 
 
 # ------------------------------------------------- the chunked form in planes
@@ -80,6 +86,33 @@ def chunked(x, h, scale, mm, keep=None, l2norm=True, eps=1e-6):
             keep.append((S, U))
         S = last * S + mm("K^T U", k.T, d * U)
     return torch.cat(out), S
+
+
+def chunked_back(x, do, h, dh, scale, mm):
+    """Gradients of one row and head, rows as given (no norms)."""
+    keep, n = [], -(-x[0].shape[1] // 64)
+    chunked(x, h, scale, mm, keep, l2norm=False)
+    dS, out = dh[0, 0].double(), []
+    for c in reversed(range(n)):
+        q, k, v, beta, e, d, D, T, A, last = factors(x, False, 0.0, scale, c)
+        S0, U = keep[c]
+        o = do[0, 64 * c:64 * c + 64, 0].double()
+        dU = mm("A^T dO", A.T, o) + d * mm("K dS", k, dS)
+        dR = mm("T^T dU", T.T, dU)
+        dA, dM = mm("dO U^T", o, U.T).tril(), -mm("dR U^T", dR, U.T).tril(-1)
+        B1, B2 = scale * D * dA, beta * D * dM
+        oS, rS, uS = mm("dO S^T", o, S0.T), mm("dR S^T", dR, S0.T), mm("U dS^T", U, dS.T)
+        dq = scale * e * oS + mm("B1 K", B1, k)
+        dk = mm("B1^T Q", B1.T, q) + mm("B2 K", B2 + B2.T, k) + d * uS - beta * e * rS
+        z = B1 * (q @ k.T) + B2 * (k @ k.T)
+        us = (d * uS * k).sum(1)
+        dG = (scale * e * oS * q).sum(1) - (beta * e * rS * k).sum(1) + z.sum(1) - z.sum(0) - us
+        dG[-1] += us.sum() + last * (S0 * dS).sum()
+        dbeta = (dR * v).sum(1) - (e * rS * k).sum(1) + (D * (k @ k.T) * dM).sum(1)
+        out.insert(0, (dq, dk, beta * dR, dG.flip(0).cumsum(0).flip(0), dbeta))
+        dS = last * dS + mm("Q^T dO", q.T, scale * e * o) - mm("K^T dR", k.T, beta * e * dR)
+    parts = [torch.cat(t) for t in zip(*out)]
+    return dict(zip(NAMES, parts + [dS]))
 
 
 def inputs(B, L, H, G, N, P, dtype, seed, held, device, raw=False):
@@ -133,6 +166,24 @@ def test_bound_of_bf16_outputs_sees_two_planes(less, L, held):
     assert (e > ACC) == (less is not None)
 
 
+PRODUCTS = ["T R", "A^T dO", "K dS", "T^T dU", "dO U^T", "dR U^T", "dO S^T", "dR S^T", "U dS^T", "B1 K", "B1^T Q", "B2 K",
+            "Q^T dO", "K^T dR"]
+
+
+@pytest.mark.parametrize("less", [None] + PRODUCTS)
+def test_bound_of_gradients_sees_two_planes(less):
+    worst = 0.0
+    for L, held in ((190, False), (130, True)):
+        x, h, do, dh = inputs(1, L, 1, 1, 64, 64, torch.float32, 31, held, "cpu", raw=True)
+        want = ref.backward(*x, do, h, dh, scale=0.3, l2norm=False)
+        got = chunked_back(x, do, h, dh, 0.3, Products(less))
+        for n in NAMES:
+            if n != "dg" or not held:   # (dg of a held state is far smaller than its terms)
+                worst = max(worst, ref.rel2(got[n], want[n][0] if n == "dh_in" else want[n][0, :, 0]))
+    say("   less %s: %.1e" % (less, worst))
+    assert (worst > GRAD_ACC) == (less is not None)
+
+
 # ------------------------------------------------------------------ the kernels
 
 FORWARD = [
@@ -158,3 +209,37 @@ def test_prefill(B, L, H, G, N, P, io, held):
     eh = ref.rel2(hL, wh)
     say("   o %.2e, h %.2e" % (eo, eh))
     assert max(eo, eh) <= ACC
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("held", [False, True])
+@pytest.mark.parametrize("B,H,G,N,P,io", [(64, 8, 8, 64, 64, "bf16"), (32, 8, 2, 128, 128, "bf16"), (64, 8, 8, 32, 96, "f32"),
+                                          (32, 4, 1, 128, 64, "f32")])
+def test_step(B, H, G, N, P, io, held):
+    from mamba_selective_ssm_amd import m3_delta_step
+    say("case step", B, H, G, N, P, io, held)
+    x, h, _, _ = inputs(B, 1, H, G, N, P, DT[io], 51, held, "cuda")
+    wo, wh = ref.forward(*x, h, scale=0.3, l2norm=True)
+    o = m3_delta_step(*[t[:, 0].contiguous() for t in x], h, l2norm=True, scale=0.3)
+    eo = rounding_error(o, wo[:, 0]) if io == "bf16" else ref.rel2(o, wo[:, 0])
+    eh = ref.rel2(h, wh)
+    say("   o %.2e, h %.2e" % (eo, eh))
+    assert max(eo, eh) <= ACC
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("held", [False, True])
+@pytest.mark.parametrize("B,L,H,G,N,P,io,l2", [
+    (2, 300, 4, 4, 64, 64, "bf16", True), (1, 200, 4, 1, 128, 128, "bf16", True), (2, 130, 6, 2, 32, 96, "bf16", False),
+    (1, 300, 4, 2, 64, 64, "f32", True), (1, 130, 2, 2, 128, 64, "f32", False), (1, 200, 3, 3, 32, 128, "f32", True),
+    (1, 130, 2, 1, 128, 128, "f32", True)])
+def test_gradient(B, L, H, G, N, P, io, l2, held):
+    from mamba_selective_ssm_amd import m3_delta_bwd
+    say("case gradient", B, L, H, G, N, P, io, l2, held)
+    x, h, do, dh = inputs(B, L, H, G, N, P, DT[io], 61, held, "cuda", raw=not l2)
+    got = m3_delta_bwd(*x, do, h, dh, scale=0.3, l2norm=l2)
+    want = ref.backward(*x, do, h, dh, scale=0.3, l2norm=l2)
+    errs = {n: ref.rel2(getattr(got, n), want[n]) for n in NAMES}
+    say("   " + " ".join("%s %.1e" % e for e in errs.items()))
+    for n, e in errs.items():
+        assert e <= GRAD_ACC or (n == "dg" and held), (n, e)
