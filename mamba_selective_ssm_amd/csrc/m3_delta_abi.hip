@@ -43,7 +43,7 @@ m3_status check_sizes(int64_t batch, int64_t seqlen, int64_t H, int64_t G, int64
     if (l2norm && !(eps >= 0.f && eps < 3.0e38f)) return M3_ERR_OPTION;
     if (!(fabsf(scale) < 3.0e38f)) return M3_ERR_OPTION;
     // offsets inside one chunk are kept in 32 bits: 64 H 128 values
-    if (H > ((int64_t)1 << 14) || batch > ((int64_t)1 << 24)) return M3_ERR_UNSUPPORTED;
+    if (H > ((int64_t)1 << 14) || G > ((int64_t)1 << 14) || batch > ((int64_t)1 << 24)) return M3_ERR_UNSUPPORTED;
     if (batch * H > ((int64_t)1 << 24)) return M3_ERR_UNSUPPORTED;
     return M3_OK;
 }
@@ -79,7 +79,7 @@ m3_status plan_delta(const m3_delta_args* a, bool train, DeltaPlan* out)
     if (train) {
         const int64_t tok = packed ? a->seqlen : a->batch * a->seqlen;   // dense: 64 chunks' worth at most
         if (a->batch >= kMaxBlocks256) return M3_ERR_UNSUPPORTED;
-        if (H > 0 && tok > 4 * (kMaxThreads - 255) / (out->G * a->dstate)) return M3_ERR_UNSUPPORTED;
+        if (out->G > 0 && tok > 4 * (kMaxThreads - 255) / (out->G * a->dstate)) return M3_ERR_UNSUPPORTED;
     }
     const int64_t slots = packed ? a->seqlen / m3::kDC + a->batch + 1 : a->batch * out->nc;
     out->chunks = slots * H;
@@ -320,10 +320,9 @@ m3_status m3_delta_bwd(const m3_delta_bwd_args* b, void* stream)
     if (s != M3_OK) return s;
     if (a->slots != nullptr || a->h_out != nullptr || a->o != nullptr) return M3_ERR_UNSUPPORTED;
     const DeltaBytes n = bytes_of(a, pl);
-    if (a->batch * a->nheads == 0 && n.vo == 0) return M3_OK;
-    if (n.vo > 0 && (!a->q || !a->k || !a->v || !a->g || !a->beta || !b->dout || !b->dq || !b->dk || !b->dv || !b->dg ||
-                     !b->dbeta))
-        return M3_ERR_NULL;
+    if (a->batch * a->nheads == 0 && n.vo == 0 && n.qk == 0) return M3_OK;
+    if (n.vo > 0 && (!a->q || !a->k || !a->v || !a->g || !a->beta || !b->dout || !b->dv || !b->dg || !b->dbeta)) return M3_ERR_NULL;
+    if (n.qk > 0 && (!b->dq || !b->dk)) return M3_ERR_NULL;   // (groups without heads: zeros)
     const void* al[] = {a->q, a->k, a->v, a->g, a->beta, a->h_in, b->dout, b->dh_out, b->dq, b->dk, b->dv, b->dg, b->dbeta,
                         b->dh_in};
     for (const void* x : al)

@@ -780,7 +780,8 @@ __global__ __launch_bounds__(256, PB <= 2 ? 2 : 1) void delta_grad_kernel(const 
     }
 }
 
-// dq and dk of a group of heads: the sum over its heads, in their order.
+// dq and dk of a group of heads: the sum over its heads, in their order (zeros
+// where it has none).
 static __global__ __launch_bounds__(256) void delta_heads_kernel(const float* eq, const float* ek, float* oq, float* ok,
                                                                   int64_t tokens, int H, int G, int N)
 {
@@ -791,8 +792,8 @@ static __global__ __launch_bounds__(256) void delta_heads_kernel(const float* eq
     const int64_t t = i / ((int64_t)G * N);
     const int j = (int)(i - t * G * N), gi = j / N, reach = H / G;
     const float* src = e + (t * H + (int64_t)gi * reach) * N + (j - gi * N);
-    f32x4 s = *reinterpret_cast<const f32x4*>(src);
-    for (int k = 1; k < reach; ++k) s += *reinterpret_cast<const f32x4*>(src + (int64_t)k * N);
+    f32x4 s = {0.f, 0.f, 0.f, 0.f};
+    for (int k = 0; k < reach; ++k) s += *reinterpret_cast<const f32x4*>(src + (int64_t)k * N);
     *reinterpret_cast<f32x4*>(out + i) = s;
 }
 
@@ -861,7 +862,7 @@ hipError_t bwd_n(const DeltaBwdParams& bp, hipStream_t stream)
     default: e = launch_delta_pre<IO, N, 4>(bp, stream);
     }
     if (e != hipSuccess) return e;
-    if (p.rows > 0) {
+    if (p.rows > 0 && p.H > 0) {
         using Cf = WalkCfg<IO, N, true>;
         auto* const walks = &delta_walks_kernel<IO, N>;
         static_assert(Cf::total <= 160 * 1024, "a workgroup's LDS");
@@ -880,7 +881,7 @@ hipError_t bwd_n(const DeltaBwdParams& bp, hipStream_t stream)
     }
     if (e != hipSuccess) return e;
     const int64_t tokens = p.cu != nullptr ? p.L : p.rows * p.L;
-    if (p.cu != nullptr && p.L > 0) {
+    if (p.cu != nullptr && p.L > 0 && p.H > 0) {
         const DeltaRest r = {{bp.dqe, bp.dke, bp.dv, bp.dg, bp.dbeta}, {p.H * p.N, p.H * p.N, p.H * p.P, p.H, p.H}};
         hipLaunchKernelGGL(delta_rest_kernel, dim3(p.rows + 1, 16), dim3(256), 0, stream, p, r);
         if ((e = hipGetLastError()) != hipSuccess) return e;
