@@ -1,14 +1,18 @@
 """Every output of the gated delta rule's gradient is written: outputs that
-hold NaN before the call, in calls without heads."""
+hold NaN before the call, tokens outside every sequence, rows longer than
+max_seqlen, and calls without heads."""
 import ctypes
 
 import pytest
 import torch
 
+import delta_reference as ref
+from helpers import say
 from mamba_selective_ssm_amd import binding, delta, m3_delta_bwd
 
 FAKE = 0x7F0000000000
 NAMES = ("dq", "dk", "dv", "dg", "dbeta", "dh_in")
+TOL = 2e-5   # as in test_delta_bwd_gpu.py
 
 
 def call(x, do, h=None, dh=None, cu=None, max_seqlen=0, scale=0.2, rows=None):
@@ -31,6 +35,49 @@ def call(x, do, h=None, dh=None, cu=None, max_seqlen=0, scale=0.2, rows=None):
     assert lib.m3_delta_bwd(ctypes.byref(b), torch.cuda.current_stream().cuda_stream) == 0
     torch.cuda.synchronize()
     return out
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("io", ["bf16", "f32"])
+@pytest.mark.parametrize("N,P,H,G", [(64, 64, 4, 4), (64, 64, 4, 2), (32, 96, 3, 1), (128, 32, 2, 2)])
+def test_tokens_outside_every_sequence(io, N, P, H, G):
+    """Gaps before the first sequence and behind the last, an empty sequence, one longer than max_seqlen: exact zeros there, the
+    gradients of the rest as if each sequence ended at max_seqlen."""
+    say("case outside", io, N, P, H, G)
+    at, T, longest = [13, 18, 18, 82, 200, 263], 280, 100   # lengths 5, 0, 64, 118 (100 of them taken), 63
+    x = ref.inputs(1, T, H, G, N, P, torch.bfloat16 if io == "bf16" else torch.float32, 321)
+    gen = torch.Generator().manual_seed(322)
+    do = torch.randn(1, T, H, P, generator=gen).to(x[0].dtype).cuda()
+    h, dh = (torch.randn(5, H, N, P, generator=gen).cuda() for _ in range(2))
+    got = call(x, do, h, dh, torch.tensor(at, dtype=torch.int32).cuda(), longest)
+    rest = torch.ones(T, dtype=torch.bool)
+    for i in range(5):
+        part = slice(at[i], min(at[i + 1], at[i] + longest))
+        rest[part] = False
+        want = ref.backward(*(t[:, part] for t in x), do[:, part], h[i:i + 1], dh[i:i + 1], scale=0.2, l2norm=True)
+        for n in NAMES:
+            g = got[n][i:i + 1] if n == "dh_in" else got[n][:, part]
+            assert bool(g.isfinite().all()), (n, i)
+            assert ref.rel2(g, want[n]) <= TOL, (n, i)
+    for n in NAMES[:5]:
+        assert bool((got[n][:, rest.cuda()] == 0).all()), n
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("G", [1, 3])
+def test_dense_outputs_and_no_sequences(G):
+    H, N, P = 3, 64, 32
+    x = ref.inputs(2, 70, H, G, N, P, torch.bfloat16, 331)
+    do = torch.randn(2, 70, H, P, generator=torch.Generator().manual_seed(332)).to(torch.bfloat16).cuda()
+    got = call(x, do)
+    want = ref.backward(*x, do, scale=0.2, l2norm=True)
+    for n in NAMES:
+        assert ref.rel2(got[n], want[n]) <= TOL, n
+    # one offset: no sequence at all
+    y = [t[:1].contiguous() for t in x]
+    got = call(y, do[:1].contiguous(), cu=torch.zeros(1, dtype=torch.int32, device="cuda"), max_seqlen=70)
+    for n in NAMES[:5]:
+        assert bool((got[n] == 0).all()), n
 
 
 @pytest.mark.gpu
