@@ -423,12 +423,15 @@ int m3_decode_supported(int64_t dstate, int64_t headdim, int64_t rank, int32_t i
  *   h        [batch, nheads, dstate, headdim]     float32: S, the state record
  * l2norm 1: every row of q and of k is used as x / sqrt(sum(x^2) + norm_eps).
  * Sizes: dstate 32, 64 or 128; headdim 32, 64, 96 or 128; ngroups 0 (one group
- * per head) or a divisor of nheads.
+ * per head) or a divisor of nheads, at most 2^14; batch * nheads * chunks of 64
+ * tokens of the longest row (packed: of max_seqlen) below 2^24.
  *
  * Options as in m3_scan_fwd:
  *   cu_seqlens, max_seqlen   packed sequences (prefill and gradient): the token
  *            arrays are [seqlen, ...] with seqlen the total, one state record
- *            per sequence; 0 <= max_seqlen <= seqlen bounds every length.
+ *            per sequence; 0 <= max_seqlen <= seqlen bounds every length (of
+ *            a longer sequence only that many tokens are taken).  A bound far
+ *            above the longest length costs empty workgroups.
  *            Tokens outside the sequences: o is left as it was, gradients are 0
  *   slots    int32 [batch] (prefill and step): row b's record is slot
  *            slots[b] of a pool of nslots records, h_in and h_out (h) are then
@@ -436,7 +439,9 @@ int m3_decode_supported(int64_t dstate, int64_t headdim, int64_t rank, int32_t i
  *            say, for a padding row) stands for no record: the row starts from
  *            zero and leaves no state.  Of several rows that name one slot the
  *            first has the record, the others' outputs are NaN.  Slots that no
- *            row names are left as they were.
+ *            row names are left as they were.  Each row looks through the
+ *            entries before its own: a cost of batch^2, which shows from some
+ *            10^4 rows on.
  * Products run on bf16 matrix cores with float32 operands split into up to
  * three bf16 values and float32 sums: states, outputs and gradients have
  * float32's accuracy for both io dtypes; a bf16 output is rounded once.  NaN and Inf inputs propagate as in
@@ -520,8 +525,9 @@ typedef struct {
 
 /* Copy: record src_slot[i] of `src` to slot dst_slot[i] of `dst`, i < count, as
  * if every source were read before any slot is written; of pairs that name one
- * slot of dst the last wins.  src_slot[i] < 0: the slot is cleared.  Pairs with
- * src_slot[i] >= src.slots or dst_slot[i] outside dst are left out.  dst may be
+ * slot of dst the last wins (a check that costs count^2; it shows from some 10^4
+ * pairs on).  src_slot[i] < 0: the slot is cleared.  Pairs with src_slot[i] >=
+ * src.slots or dst_slot[i] outside dst are left out.  dst may be
  * src (all arrays the same): then a workspace of m3_pool_copy_workspace_bytes
  * is needed; any other overlap is refused. */
 typedef struct {
@@ -534,8 +540,9 @@ typedef struct {
 
 /* Fork: for each parents[i], in order, the lowest free slot gets a copy of
  * record parents[i] (< 0: a cleared record) and is marked live; children[i] is
- * that slot, or -1 where no slot is left or the parent is not live.  live_out
- * may be live.  Workspace: 4 * count bytes. */
+ * that slot, or -1 where no slot is left or the parent was not live before the
+ * call (children are no parents of the same call's).  live_out may be live.
+ * Workspace: 4 * count bytes. */
 typedef struct {
     m3_pool pool;
     const int32_t *live;

@@ -84,17 +84,18 @@ constexpr bool delta_supported(int64_t N, int64_t P, int io_dtype)
 // Long prefills whose walk leaves CUs idle are walked in parts, each beside the
 // chunk matrices of the next, which the walk then reads out of the caches.  Whole
 // calls, us, at once / in parts, P = 64, bf16: 65536 tokens, 128 slices, N = 128:
-// 2092 / 1830; 16384: 553 / 471; 8192: 268 / 236; 4096: 120 / 118; N = 64, 65536
-// tokens, 32 slices: 1594 / 1162, 64: 1700 / 1305; 8192, 192: 296 / 253; at 256
-// slices no CU is left: 1182 / 1238.
+// 2105 / 1945; 16384: 553 / 500; 8192: 272 / 246; 4096: 128 / 125; N = 64, 65536
+// tokens, 32 slices: 1598 / 1215, 64: 1710 / 1382; 8192, 192: 302 / 249.  At 256
+// slices no CU is left over and it goes either way: N = 64, 32768 tokens: 1208 /
+// 1133, 8192: 327 / 297; N = 128, 16384: 679 / 707, 8192: 353 / 359.
 // A part is as many chunks as leave its rows and matrices in the caches together
 // with the next one's, about 1024 chunks and heads in bf16: 32 heads, N = 128,
-// parts of 16 / 32 / 48 / 64 / 128 chunks: 1851 / 1830 / 1941 / 1988 / 1985 us;
-// float32, 16 heads, N = 64, 16384 tokens: 641 / 595 / 625 / 638 (at once: 751).
-// It has to be long beside a launch and the walk's first loads, 32 chunks at
-// least: 16 heads, N = 64, 16384 tokens: 348 / 303 / 295 / 284 (at once: 289).
-// Calls of two such parts or less lie in the caches as they are: 1 head, N = 64,
-// 32768 tokens: 492 / 525; 16 heads, float32, 4096: 164 / 167.
+// parts of 16 / 32 / 48 / 64 / 128 chunks: 1927 / 1949 / 2005 / 2024 / 2024 us;
+// float32, 16 heads, N = 64, 16384 tokens: 646 / 606 / 607 / 630 / 721 (at once:
+// 731).  It has to be long beside a launch and the walk's first loads, 32 chunks
+// at least: 16 heads, N = 64, 16384 tokens: 375 / 342 / 330 / 311 / 311 (at once:
+// 313).  Calls of two such parts or less lie in the caches as they are: 1 head, N
+// = 64, 32768 tokens: 542 / 573; 16 heads, float32, 4096: 162 / 167.
 constexpr int64_t delta_part_size(int io_dtype) { return io_dtype == 0 ? 512 : 1024; }
 constexpr int64_t delta_part(int64_t units, int io_dtype)
 {
@@ -167,8 +168,8 @@ __device__ __forceinline__ DeltaRow delta_row(const DeltaParams& p, int b)
 
 // Row and head of a walk's workgroup.  The rows with the most chunks come first:
 // a CU whose last workgroup is a long one holds up the call.  13 sequences of 7
-// to 40 chunks, 32 heads, N = P = 128: 314 us for 402; the gradient's walks, 7
-// sequences of 4099 tokens in all, 16 heads: 67 for 71.
+// to 40 chunks, 32 heads, N = P = 128: calls of 552 us for 586 one at a time; the
+// gradient, 7 sequences of 4099 tokens in all, 16 heads: 244 for 254.
 __device__ __forceinline__ void delta_unit(const DeltaParams& p, int64_t unit, int& b, int& h)
 {
     int64_t b64, h64;
@@ -278,7 +279,7 @@ __device__ __forceinline__ bf16x8 join8(const bf16x4& a, const bf16x4& b)
 // upper half of what those before it left.  More instructions than planes8, of a
 // kind that the state waves beside do not wait for: delta_wide's output waves
 // with planes8 / this: 166 / 157 us (N = 64, P = 96, 96 rows and heads, 2048
-// tokens); delta_walk's, whose time is the way from LDS to the product: 78 / 82
+// tokens); delta_walk's, whose time is the way from LDS to the product: 80 / 82.5
 // (N = P = 64, 64 of them).
 __device__ __forceinline__ void cut8(const f32x4& a, const f32x4& b, bf16x8 (&o)[3])
 {

@@ -387,7 +387,7 @@ __device__ __forceinline__ void delta_back(const DeltaBwdParams& bp, int64_t bid
 
 // Both walks of the gradient: neither needs the other, and each alone waits
 // for its own chain most of the time.  All workgroups of one, then of the
-// other, so that a CU gets one of each.  78 us at 256 slices, 32 chunks, N = P =
+// other, so that a CU gets one of each.  79 us at 256 slices, 32 chunks, N = P =
 // 64 (107 as two launches), about 156 KB of memory traffic a chunk and head
 // (4.1 TB/s).
 template <typename IO, int N>
@@ -417,7 +417,7 @@ template <typename IO, int N, int PB> struct GradCfg {
 // four waves, the next tile's loads in flight; then U takes that place, then
 // B1 and B2, whose columns dk needs.  Bound by memory: a chunk's two states, U,
 // dR and its rows come in once, 64 KB of gradients go out; 144 KB a chunk and
-// head at N = P = 64, 90 us for 2048 of them (3.3 TB/s) with two workgroups to a
+// head at N = P = 64, 93 us for 2048 of them (3.2 TB/s) with two workgroups to a
 // CU.  With a lane for four rows instead of one (products not transposed) the
 // factors, sums and stores were four times as many: 193 us.
 template <typename IO, int N, int PB>

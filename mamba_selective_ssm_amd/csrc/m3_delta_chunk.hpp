@@ -82,13 +82,13 @@ template <int LD, typename F> __device__ __forceinline__ void each_lower(const f
 // sums keeps float32's relative precision after a token whose decay is near
 // zero.  Rows past the end read the last row again; their beta is 0 and their
 // g is 0, which makes their rows of T the identity's.
-// Bound by memory: at N = 64 in bf16 16 KB of rows come in and 31 KB of T, A
-// and factors go out per chunk and head, 63 KB at N = 128.  20 us for 2048
+// Bound by memory: at N = 64 in bf16 16 KB of rows come in and 31 KB of T (three
+// planes), A (float32) and factors go out per chunk and head, 63 KB at N = 128.  20 us for 2048
 // chunks and heads at N = 64 (4.7 TB/s), 424 us for 32768 at N = 128 (4.9
 // TB/s), 16 us for the gradient's 28 KB each (2048; 3.6 TB/s).  A workgroup of
 // four wavefronts with shared rows and barriers took 40 and 750 us.  Without A,
 // which the walk would then make, 15.6 and 246 us; but the walk lost more (56
-// for 39 and 1980 for 1660 us).
+// for its 39 of then and 1980 for 1660 us).
 constexpr int kChunkLds = (64 * 68 + 5 * 64) * 4;   // bytes
 template <typename IO, int N, bool BWD>
 __device__ __forceinline__ void delta_chunk(const DeltaParams& p, int64_t bid, char* lds)

@@ -59,16 +59,16 @@ hipError_t launch_delta_parts(const DeltaParams& p, hipStream_t stream)
 
 // Which walk.  A slice is 16 columns of one row and head.  Up to one slice per
 // CU its chain of products is the call's time, and four wavefronts on one slice
-// (delta_walk) take less than one wavefront's registers (delta_wide): 39 against
-// 53 us at 256 slices, 2048 tokens, N = 64.  With more, a CU's LDS reads are,
-// and delta_wide has a quarter of them (whole calls over 2048 tokens, us, P =
-// 64, delta_walk / delta_wide): N = 64: 288 slices 104 / 100, 384: 112 / 107,
-// 512: 128 / 118, 768: 264 / 186, 1024: 337 / 230; N = 32, 512: 113 / 97; N =
-// 128, 288: 130 / 125, 512: 183 / 162, 1024: 368 / 266.  Where P allows, 64
+// (delta_walk) take less than one wavefront's registers (delta_wide): 72 against
+// 94 us a call at 256 slices, 2048 tokens, N = 64.  With more, a CU's LDS reads
+// are, and delta_wide has a quarter of them (whole calls over 2048 tokens, us, P =
+// 64, delta_walk / delta_wide): N = 64: 288 slices 118 / 107, 384: 123 / 111,
+// 512: 136 / 123, 768: 261 / 189, 1024: 334 / 228; N = 32, 512: 116 / 98; N =
+// 128, 288: 139 / 123, 512: 185 / 155, 1024: 369 / 269.  Where P allows, 64
 // columns go to a workgroup above 512 slices: with 32 of them such calls are two
-// rounds over the chip or more (N = 64: 544 slices 185 for 128, 768: 245 for
-// 186, 1024: 281 for 230; N = 128, 1024: 309 for 266).  Up to there half of the
-// CUs would be idle with 64 (N = 128, 512 slices: 166 for 162).
+// rounds over the chip or more (N = 64: 544 slices 170 for 142, 768: 231 for
+// 189, 1024: 264 for 228; N = 128, 1024: 314 for 269).  Up to there half of the
+// CUs would be idle with 64 (N = 64, 512 slices: 137 for 123; N = 128: 173 for 155).
 template <typename IO, int N>
 hipError_t fwd_n(const DeltaParams& p, hipStream_t stream)
 {

@@ -11,9 +11,14 @@
 // rg N/8 .. +N/8-1 of columns 4 cq .. +3, so its k and q values are contiguous
 // too.  All its loads are in flight at once (N/8 of 16 bytes a lane), and the
 // only exchange is the sum over the eight row groups.
-// 256 rows x 32 heads, N = 128, P = 64: 537 MB of state in 96 us, 5.6 TB/s (a
-// copy of 4 GiB runs at 4.7).  Loads that bypass the caches took 108 us, one or
-// two wavefronts to a workgroup instead of four 102 and 98.
+// 256 rows x 32 heads, N = 128, P = 64, 537 MB of state read and written: calls in
+// turn on four states 110 us, 4.9 TB/s (a copy of 4 GiB runs at 4.7); one after the
+// other on one, part of which then lies in the caches, 84.  Loads that bypass the
+// caches: 108 and 85, one or two wavefronts to a workgroup instead of four: 113 and
+// 88, 113 and 85.
+// A row in a slot first looks for its slot in all earlier rows' entries, beside its
+// loads: 2 us of 51 at 256 rows, 15 of 229 at 4096, 260 of 1109 at 16384 (8 heads, N
+// = P = 64).
 #include "m3_delta.hpp"
 
 namespace m3 {

@@ -31,21 +31,21 @@ namespace m3 {
 //     tiles 0, 1 and 2, 3, the splits held up the state's: 83 for 78 us a call at
 //     256 slices, 1990 for 1935 at 128.
 // Three buffers (two chunks ahead) for the forward bf16 walk: with two the 256
-// slices below take 5 us more, N = 128 over 65536 tokens 2098 -> 2503 us.
+// slices below take 5 us more, a call of N = 128 over 65536 tokens 2267 us for 1945.
 //
-// A chunk takes about 2300 cycles at N = 64, LDS busy for 1090 of them and
-// waiting on bank conflicts for 310; 3170, 1470 and 460 at N = 128.  Over 32
-// chunks, 256 slices: 39 us (N = 64); over 1024 chunks, 128 slices at N = 128:
-// 1660 us.  The first kernel, one workgroup of four wavefronts that loaded
-// and computed in turn, took 110 and 4730 us.
+// A chunk takes 2700 cycles at N = 64, LDS busy for 1120 of them and waiting on
+// bank conflicts for 280; 3590, 1540 and 420 at N = 128.  Over 32 chunks, 256
+// slices: 42 us (N = 64); over 1024 chunks, 128 slices at N = 128: 1665 us.  The
+// first kernel, one workgroup of four wavefronts that loaded and computed in turn,
+// took 110 and 4730 us.
 //
 // K rows lie in LDS in blocks of 8 values whose place is permuted by the row
 // (k_block), which keeps both the row-wise and the transposed reads free of
 // bank conflicts without padding, as the direct loads need it.
 // TRAIN (the gradient's two walks, which run beside each other): no output
-// wavefronts, and buffers for one chunk ahead only, so that two workgroups fit
-// on a CU: 90 us for both walks at 256 slices each (N = P = 64, 32 chunks), 102
-// to 113 us with two chunks ahead and one workgroup to a CU.
+// wavefronts, and buffers for one chunk ahead only, so that two workgroups fit on
+// a CU at N = 128 too: 79 us for both walks at 256 slices each (N = P = 64, 32
+// chunks), where two chunks ahead fit as well and take 81.
 template <typename IO, int N, bool TRAIN> struct WalkCfg {
     static constexpr int KP = DeltaPlanes<IO>::io, WP = DeltaPlanes<IO>::wide;
     static constexpr bool DIRECT = KP == 1;           // io values are operands as they are: loads go straight to LDS

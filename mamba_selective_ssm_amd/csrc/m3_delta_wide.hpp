@@ -16,14 +16,14 @@ namespace m3 {
 // factors serves NS of them.  The state waves leave S and U for
 // four output waves, each with two row tiles of half the column groups (all
 // groups of one tile read twice as much LDS, and buffers twice as large left no
-// room for NS = 4 at N = 128: 508 for 375 us there, below); Q S beside R and U,
+// room for NS = 4 at N = 128, a third more there); Q S beside R and U,
 // A U beside the state's product, two barriers a chunk.  bf16 calls only: K's
 // planes of a float32 call would leave no room.
-// 8 x 32 heads x 2048 tokens, P = 64: 230 us a call at N = 64 (delta_walk 337),
-// of which 150 are this kernel's; 266 at N = 128 (368), where its 650 MB move at
-// 4 TB/s.  13 packed sequences of 20011 tokens, 32 heads, N = P = 128: 375 us,
-// 5 us a chunk and CU: matrix cores busy for 33% of them, vector units 31%, LDS
-// 31% and 10% in bank conflicts, the chain's waits the rest.
+// 8 x 32 heads x 2048 tokens, P = 64: 228 us a call at N = 64 (delta_walk 334),
+// of which 134 are this kernel's; 269 at N = 128 (369), of which 152: 660 MB at 4.3
+// TB/s, 8850 cycles a chunk and CU, matrix cores busy for 39% of them, vector units
+// 40%, LDS 35% and 10% in bank conflicts.  13 packed sequences of 20011 tokens, 32
+// heads, N = P = 128: 345 to 370 us.
 template <int N, int NS> struct WideCfg {
     static constexpr int WP = DeltaPlanes<bf16>::wide;
     static constexpr int KB = N / 32, NT = N / 16, waves = NS + 5;

@@ -11,8 +11,9 @@ N is 32, 64 or 128, P is 32, 64, 96 or 128, H a multiple of G; float32 or
 bfloat16 tokens.
 
 Options: scale (default N ** -0.5); l2norm: rows of q and k divided by
-sqrt(sum of squares + norm_eps); cu_seqlens (int32 [nseq + 1]) and max_seqlen:
-sequences packed along the token axis of [1, T, ...] arrays; slots (int32, one
+sqrt(sum of squares + norm_eps); cu_seqlens (int32 [nseq + 1]) and max_seqlen
+(default T; batch * heads * max_seqlen / 64 has to stay below 2^24): sequences
+packed along the token axis of [1, T, ...] arrays; slots (int32, one
 per row): row b's record is slot slots[b] of a pool h [slots, H, N, P], read
 and written in place.
 """

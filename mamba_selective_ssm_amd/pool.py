@@ -96,7 +96,8 @@ def m3_pool_fork(pool, live: torch.Tensor, parents: torch.Tensor, *,
                  workspace: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """For each parents[i] the lowest free slot, a copy of that record (< 0: a
     cleared one) in it, marked in ``live_out`` (default: ``live`` itself).
-    Returns the slots, -1 where none was left or the parent is not live."""
+    Returns the slots, -1 where none was left or the parent was not live before
+    the call."""
     slots, dev, d = _desc(pool, "pool")
     n = parents.numel()
     live_out = live if live_out is None else live_out
