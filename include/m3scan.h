@@ -423,15 +423,15 @@ int m3_decode_supported(int64_t dstate, int64_t headdim, int64_t rank, int32_t i
  *   h        [batch, nheads, dstate, headdim]     float32: S, the state record
  * l2norm 1: every row of q and of k is used as x / sqrt(sum(x^2) + norm_eps).
  * Sizes: dstate 32, 64 or 128; headdim 32, 64, 96 or 128; ngroups 0 (one group
- * per head) or a divisor of nheads, at most 2^14; batch * nheads * chunks of 64
- * tokens of the longest row (packed: of max_seqlen) below 2^24.
+ * per head) or a divisor of nheads, at most 2^14; nheads times the chunks of 64
+ * tokens (batch times a row's; packed: seqlen / 64 + batch + 1) below 2^24;
+ * gradient: tokens * groups * dstate below 2^34.
  *
  * Options as in m3_scan_fwd:
  *   cu_seqlens, max_seqlen   packed sequences (prefill and gradient): the token
  *            arrays are [seqlen, ...] with seqlen the total, one state record
  *            per sequence; 0 <= max_seqlen <= seqlen bounds every length (of
- *            a longer sequence only that many tokens are taken).  A bound far
- *            above the longest length costs empty workgroups.
+ *            a longer sequence only that many tokens are taken).
  *            Tokens outside the sequences: o is left as it was, gradients are 0
  *   slots    int32 [batch] (prefill and step): row b's record is slot
  *            slots[b] of a pool of nslots records, h_in and h_out (h) are then

@@ -50,6 +50,7 @@ m3_status check_sizes(int64_t batch, int64_t seqlen, int64_t H, int64_t G, int64
 
 struct DeltaPlan {
     int64_t G, nc, chunks;     // q/k groups; chunks of the longest row; (chunk slot, head) entries
+    int64_t places;            // DeltaParams::places
     size_t tri_w, tri_o, sc;   // bytes of one array of each kind
     size_t st, rowsP, heads;   // gradient: states, [64][P] rows, per-head dq or dk
     size_t order;              // packed rows in the walks' order
@@ -70,7 +71,12 @@ m3_status plan_delta(const m3_delta_args* a, bool train, DeltaPlan* out)
     if (longest > ((int64_t)1 << 30) || a->seqlen > ((int64_t)1 << 38)) return M3_ERR_UNSUPPORTED;
     out->G = a->ngroups > 0 ? a->ngroups : H;
     out->nc = (longest + m3::kDC - 1) / m3::kDC;
-    if (a->batch > 0 && H > 0 && out->nc > kMaxBlocks256 / (a->batch * H)) return M3_ERR_UNSUPPORTED;
+    const int64_t slots = packed ? a->seqlen / m3::kDC + a->batch + 1 : a->batch * out->nc;
+    // long prefills of few rows in parts
+    out->parts = m3::delta_in_parts(a->batch * H, out->nc, a->headdim, a->io_dtype);
+    const int64_t direct = a->batch * out->nc, most = H > 0 ? kMaxBlocks256 / H : direct;
+    out->places = packed && (direct > 2 * slots || direct > most) && (train || !out->parts) ? slots : 0;
+    if ((out->places > 0 ? slots : direct) > most) return M3_ERR_UNSUPPORTED;
     // the walks: 16 columns of one row and head to a workgroup, 512 threads
     // (bf16: so few in one workgroup only where there are few, else 32 columns,
     // 448 threads), or twice 320; the other kernels that the gradient adds
@@ -81,7 +87,6 @@ m3_status plan_delta(const m3_delta_args* a, bool train, DeltaPlan* out)
         if (a->batch >= kMaxBlocks256) return M3_ERR_UNSUPPORTED;
         if (out->G > 0 && tok > 4 * (kMaxThreads - 255) / (out->G * a->dstate)) return M3_ERR_UNSUPPORTED;
     }
-    const int64_t slots = packed ? a->seqlen / m3::kDC + a->batch + 1 : a->batch * out->nc;
     out->chunks = slots * H;
     const size_t n = (size_t)out->chunks;
     out->tri_w = up256(n * m3::kTriValues * 3 * 2);   // three bf16 planes
@@ -95,7 +100,6 @@ m3_status plan_delta(const m3_delta_args* a, bool train, DeltaPlan* out)
     // so many rows leave no CU idle for long)
     out->order = packed && a->batch <= 16384 ? up256((size_t)a->batch * 4) : 0;
     // (sized for any max_seqlen)
-    out->parts = m3::delta_in_parts(a->batch * H, out->nc, a->headdim, a->io_dtype);
     out->carry = m3::delta_in_parts(a->batch * H, (a->seqlen + m3::kDC - 1) / m3::kDC, a->headdim, a->io_dtype)
                      ? up256((size_t)(a->batch * H * a->dstate * a->headdim) * 4)
                      : 0;
@@ -134,6 +138,7 @@ m3::DeltaParams params_of(const m3_delta_args* a, const DeltaPlan& pl)
     p.N = (int)a->dstate; p.P = (int)a->headdim;
     p.scale = a->scale; p.eps = a->norm_eps; p.l2norm = a->l2norm;
     p.nc = (int)pl.nc;
+    p.places = pl.places;
     return p;
 }
 

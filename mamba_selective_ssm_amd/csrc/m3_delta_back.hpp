@@ -54,7 +54,8 @@ __global__ __launch_bounds__(256) void delta_pre_kernel(const DeltaBwdParams bp)
     const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int64_t bid = blockIdx.x;
     const int h = (int)(bid % p.H), bc = (int)(bid / p.H);
-    const int c = bc % p.nc, b = bc / p.nc;
+    int b, c;
+    delta_place(p, bc, b, c);
     const DeltaRow row = delta_row(p, b);
     if ((int64_t)c * kDC >= row.len) return;
     const int64_t t0 = row.start + (int64_t)c * kDC, ci = (row.slot0 + c) * p.H + h;
@@ -442,7 +443,8 @@ __global__ __launch_bounds__(256, PB <= 2 ? 2 : 1) void delta_grad_kernel(const 
     const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int64_t bid = blockIdx.x;
     const int h = (int)(bid % p.H), bc = (int)(bid / p.H);
-    const int c = bc % p.nc, b = bc / p.nc;
+    int b, c;
+    delta_place(p, bc, b, c);
     const DeltaRow row = delta_row(p, b);
     if ((int64_t)c * kDC >= row.len) return;
     const int64_t t0 = row.start + (int64_t)c * kDC, ci = (row.slot0 + c) * p.H + h;
@@ -828,7 +830,7 @@ hipError_t launch_delta_pre(const DeltaBwdParams& bp, hipStream_t stream)
     static std::atomic<uint64_t> done{0};
     const hipError_t attr = delta_allow_lds(kern, lds, done);
     if (attr != hipSuccess) return attr;
-    const int64_t blocks = (int64_t)bp.f.rows * bp.f.nc * bp.f.H;
+    const int64_t blocks = delta_chunk_count(bp.f) * bp.f.H;
     if (blocks == 0) return hipSuccess;
     hipLaunchKernelGGL(kern, dim3((unsigned)blocks), dim3(256), lds, stream, bp);
     return hipGetLastError();
@@ -843,7 +845,7 @@ hipError_t launch_delta_grad(const DeltaBwdParams& bp, hipStream_t stream)
     static std::atomic<uint64_t> done{0};
     const hipError_t attr = delta_allow_lds(kern, lds, done);
     if (attr != hipSuccess) return attr;
-    const int64_t blocks = (int64_t)bp.f.rows * bp.f.nc * bp.f.H;
+    const int64_t blocks = delta_chunk_count(bp.f) * bp.f.H;
     if (blocks == 0) return hipSuccess;
     hipLaunchKernelGGL(kern, dim3((unsigned)blocks), dim3(256), lds, stream, bp);
     return hipGetLastError();

@@ -101,8 +101,9 @@ __device__ __forceinline__ void delta_chunk(const DeltaParams& p, int64_t bid, c
     const int lane = threadIdx.x & 63, l = lane & 15, g = lane >> 4;
     const int h = (int)(bid % p.H);
     const int bc = (int)(bid / p.H);
-    const int c = bc % p.nc, b = bc / p.nc;
-    if (c == 0 && h == 0 && p.from == 0 && p.order != nullptr) delta_rank(p, b, lane);
+    int b, c;
+    delta_place(p, bc, b, c);
+    if (bid < p.rows && p.from == 0 && p.order != nullptr) delta_rank(p, (int)bid, lane);   // (as many as rows run, at least)
     const DeltaRow row = delta_row(p, b);
     if ((int64_t)c * kDC >= row.len) return;
     const int64_t t0 = row.start + (int64_t)c * kDC;
@@ -349,7 +350,7 @@ __global__ __launch_bounds__(64, 2) void delta_chunk_kernel(const DeltaParams p)
 template <typename IO, int N, bool BWD>
 hipError_t launch_delta_chunks(const DeltaParams& p, hipStream_t stream)
 {
-    const int64_t blocks = (int64_t)p.rows * p.nc * p.H;
+    const int64_t blocks = delta_chunk_count(p) * p.H;
     if (blocks == 0) return hipSuccess;
     hipLaunchKernelGGL((delta_chunk_kernel<IO, N, BWD>), dim3((unsigned)blocks), dim3(64), 0, stream, p);
     return hipGetLastError();

@@ -12,8 +12,8 @@ bfloat16 tokens.
 
 Options: scale (default N ** -0.5); l2norm: rows of q and k divided by
 sqrt(sum of squares + norm_eps); cu_seqlens (int32 [nseq + 1]) and max_seqlen
-(default T; batch * heads * max_seqlen / 64 has to stay below 2^24): sequences
-packed along the token axis of [1, T, ...] arrays; slots (int32, one
+(a bound of the lengths, default T): sequences packed along the token axis of
+[1, T, ...] arrays; slots (int32, one
 per row): row b's record is slot slots[b] of a pool h [slots, H, N, P], read
 and written in place.
 """
