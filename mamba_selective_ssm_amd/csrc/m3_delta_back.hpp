@@ -22,7 +22,7 @@
 namespace m3 {
 
 // Sum over the four lane groups (g).
-__device__ __forceinline__ float groups_sum(float v)
+template <typename T> __device__ __forceinline__ T groups_sum(T v)
 {
     v += __shfl_xor(v, 16);
     v += __shfl_xor(v, 32);
@@ -407,7 +407,8 @@ template <typename IO, int N, int PB> struct GradCfg {
     static constexpr int q = KP * 64 * LK * 2, x = 2 * q, tile = WP * 16 * LP * 2, xs = 4 * tile, xu = WP * 64 * LP * 2,
                          xb = 2 * 64 * LB * 4;
     static constexpr int xmax = xs > xu ? (xs > xb ? xs : xb) : (xu > xb ? xu : xb);
-    static constexpr int f = x + xmax, total = f + (9 * 64 + 4 * 64 + 64 + 64 + 4) * 4;
+    static constexpr int f = x + xmax, total = f + (9 * 64 + 64 + 4) * 4 + (4 * 64 + 64) * 8;
+    static_assert(f % 8 == 0, "float64 values behind 9 rows of 64 factors");
 };
 
 // Every gradient of one chunk of one head.  Wave w has tokens 16 w .. + 15:
@@ -435,9 +436,9 @@ __global__ __launch_bounds__(256, PB <= 2 ? 2 : 1) void delta_grad_kernel(const 
     float* sB2 = sB1 + 64 * LB;
     float* sF = reinterpret_cast<float*>(glds + Cf::f);   // [8][64] factors, [64] 1/|q|
     float* sRq = sF + 8 * 64;
-    float* sCol = sRq + 64;    // [4][64] column sums of each wave's rows
-    float* sG = sCol + 256;    // [64] dG but for the column sums and the total
-    float* sUs = sG + 64;      // [64] what the factor d adds to G_last and takes from G
+    double* sCol = reinterpret_cast<double*>(sRq + 64);   // [4][64] column sums of each wave's rows
+    double* sG = sCol + 256;   // [64] dG but for the column sums and the total
+    float* sUs = reinterpret_cast<float*>(sG + 64);       // [64] what the factor d adds to G_last and takes from G
     float* sTot = sUs + 64;    // [4] each wave's share of <S0, dS1>
     const int tid = threadIdx.x, lane = tid & 63, l = lane & 15, g = lane >> 4;
     const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -628,12 +629,15 @@ __global__ __launch_bounds__(256, PB <= 2 ? 2 : 1) void delta_grad_kernel(const 
     __syncthreads();
 
     // B1, B2 (this token's row, keys 16 ct + 4 g + r), the row and column sums
-    // of Z = B1 (q.k) + B2 (k.k), and the M part of dbeta
-    float zrow = 0.f, mrow = 0.f;
+    // of Z = B1 (q.k) + B2 (k.k), and the M part of dbeta.  A key's column takes
+    // from dg what the tokens' rows gave, so both are summed in float64: dg's error
+    // was 3.3e-7 with float32 sums and is 1.7e-7, for 1% of the call.
+    double zrow = 0.;
+    float mrow = 0.f;
     f32x4 v1[4], v2[4];
 #pragma unroll
     for (int ct = 0; ct < 4; ++ct) {
-        f32x4 zc = fz;
+        double zc[4] = {0., 0., 0., 0.};
         v1[ct] = fz;
         v2[ct] = fz;
         if (ct <= w) {   // wave-uniform
@@ -678,8 +682,10 @@ __global__ __launch_bounds__(256, PB <= 2 ? 2 : 1) void delta_grad_kernel(const 
             }
         }
 #pragma unroll
-        for (int r = 0; r < 4; ++r) zc[r] = lane_group_sum<16>(zc[r]);
-        if (l == 0) *reinterpret_cast<f32x4*>(sCol + w * 64 + 16 * ct + 4 * g) = zc;
+        for (int r = 0; r < 4; ++r) {
+            zc[r] = lane_group_sum_d(zc[r]);
+            if (l == 0) sCol[w * 64 + 16 * ct + 4 * g + r] = zc[r];
+        }
     }
     zrow = groups_sum(zrow);
     mrow = groups_sum(mrow);
@@ -691,7 +697,7 @@ __global__ __launch_bounds__(256, PB <= 2 ? 2 : 1) void delta_grad_kernel(const 
     }
     // dbeta and dG of this token
     if (g == 0) {
-        sG[irow] = qs - beta * ks + zrow - us;
+        sG[irow] = (double)qs - (double)beta * ks + zrow - us;
         sUs[irow] = us;
         if (real) bp.dbeta[(t0 + irow) * p.H + h] = drv - ks + mrow;
     }
@@ -773,7 +779,7 @@ __global__ __launch_bounds__(256, PB <= 2 ? 2 : 1) void delta_grad_kernel(const 
         }
     }
     if (w == 0) {
-        double x = (double)sG[lane] - ((double)sCol[lane] + sCol[64 + lane] + sCol[128 + lane] + sCol[192 + lane]);
+        double x = sG[lane] - (sCol[lane] + sCol[64 + lane] + sCol[128 + lane] + sCol[192 + lane]);
         const double u = wave_inclusive_sum_d((double)sUs[lane]);
         if (lane == 63) x += u + (double)sF[256] * ((double)sTot[0] + sTot[1] + sTot[2] + sTot[3]);
         const double s = wave_inclusive_sum_d(x);

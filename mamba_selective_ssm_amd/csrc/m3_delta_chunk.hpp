@@ -42,6 +42,16 @@ __device__ __forceinline__ double wave_inclusive_sum_d(double v)
     return v;
 }
 
+// Sum over each 16 lanes in float64, by the lane moves of lane_group_sum.
+__device__ __forceinline__ double lane_group_sum_d(double v)
+{
+    v += dpp_moved_d<0xB1, 0xf>(v);
+    v += dpp_moved_d<0x4E, 0xf>(v);
+    v += dpp_moved_d<0x141, 0xf>(v);
+    v += dpp_moved_d<0x140, 0xf>(v);
+    return v;
+}
+
 // The operand blocks of a lower triangular matrix in LDS: block (w, kb) has
 // rows tile_row(w, l), columns 32 kb + 8 g ..+7; zero above the diagonal.  f(block,
 // its two halves of 4 columns).

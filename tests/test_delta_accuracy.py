@@ -228,6 +228,24 @@ def test_step(B, H, G, N, P, io, held):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("L,N,P,io", [(64, 64, 64, "bf16"), (17, 32, 32, "f32"), (50, 128, 128, "bf16"), (33, 64, 96, "f32")])
+def test_decay_of_the_zero_state_has_no_gradient(L, N, P, io):
+    """The first token's decay acts on a state of zeros: its dg is a sum over one chunk whose terms, each a product of float32
+    values, cancel in pairs.  The pairs are equal bit for bit, so what is left is the sums' own rounding: at most L^2 = 2^12
+    terms of 2^-53 each, 2^-41 of their sizes' sum, which is of the size of the 64 other values; asked for as 2^-36 of their
+    root mean square."""
+    from mamba_selective_ssm_amd import m3_delta_bwd
+    x, _, do, _ = inputs(2, L, 4, 2, N, P, DT[io], 71, False, "cuda")
+    got = m3_delta_bwd(*x, do, l2norm=True, scale=0.3)
+    dg = got.dg.double()
+    worst = float(dg[:, 0].abs().max() / dg.pow(2).mean().sqrt())
+    say("   %.1e of the others" % worst)
+    assert worst <= 2.0 ** -36
+    # the others are what they should be
+    assert ref.rel2(got.dg, ref.backward(*x, do, scale=0.3, l2norm=True)["dg"]) <= GRAD_ACC
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("held", [False, True])
 @pytest.mark.parametrize("B,L,H,G,N,P,io,l2", [
     (2, 300, 4, 4, 64, 64, "bf16", True), (1, 200, 4, 1, 128, 128, "bf16", True), (2, 130, 6, 2, 32, 96, "bf16", False),
