@@ -419,7 +419,7 @@ template <typename IO, int N, int PB> struct GradCfg {
 // four waves, the next tile's loads in flight; then U takes that place, then
 // B1 and B2, whose columns dk needs.  Bound by memory: a chunk's two states, U,
 // dR and its rows come in once, 64 KB of gradients go out; 144 KB a chunk and
-// head at N = P = 64, 93 us for 2048 of them (3.2 TB/s) with two workgroups to a
+// head at N = P = 64, 95 us for 2048 of them (3.1 TB/s) with two workgroups to a
 // CU.  With a lane for four rows instead of one (products not transposed) the
 // factors, sums and stores were four times as many: 193 us.
 template <typename IO, int N, int PB>
